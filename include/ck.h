@@ -53,7 +53,7 @@ typedef enum {
     CK_ERR_TIMEOUT = 6        /* written to *dev_status by a kernel whose wait expired    */
 } ck_status;
 
-typedef enum { CK_F32 = 0, CK_F16 = 1, CK_BF16 = 2, CK_I8 = 3 } ck_dtype;
+typedef enum { CK_F32 = 0, CK_F16 = 1, CK_BF16 = 2, CK_I8 = 3, CK_FP4 = 4 } ck_dtype;
 
 /*
  * Stage 1: group-wise rotation, then row-wise signed-INT4 quantization with codes
@@ -263,6 +263,115 @@ ck_status ck_rotate_quant_packed(const void* x, ck_dtype x_dtype, int64_t M, int
                                  const float* scale_in, int stochastic, uint64_t seed,
                                  uint64_t offset, uint8_t* packed, int64_t ld_packed,
                                  float* scales, cudaStream_t stream);
+
+/*
+ * Microscaled 4-bit floating point.  Elements are E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives; the sign is bit 3 of the code), two to a byte with the even k in the low nibble.
+ * Consecutive elements along K form blocks that share a scale byte:
+ *   CK_MXFP4  32 elements; E8M0, 2^(byte - 127), 255 = NaN (OCP Microscaling Formats v1.0)
+ *   CK_NVFP4  16 elements; E4M3, 0x7F = NaN, and one fp32 scale t for the whole tensor
+ * An element stands for code * scale (CK_MXFP4) or code * scale * t (CK_NVFP4).
+ *
+ * Scale bytes are kept in tiles of 128 rows x 4 blocks, 512 bytes each, the order that the tensor
+ * cores take: row r, block c of a tile at byte (r % 32) * 16 + (r / 32) * 4 + c; the tile of rows
+ * 128 i.. and blocks 4 j.. at byte (i * ceil(blocks / 4) + j) * 512.  With rows sorted by expert
+ * (offsets, below) expert e's rows start a tile row of their own, i = offsets[e] / 128 + e.
+ * Scale pointers are 16-byte aligned.
+ */
+typedef enum { CK_MXFP4 = 0, CK_NVFP4 = 1 } ck_fp4_format;
+
+/* Bytes of the scale tiles of (M, K); n_experts 0: one matrix, otherwise rows sorted by expert.
+ * Returns 0 for invalid sizes. */
+size_t ck_fp4_scales_bytes(int64_t M, int64_t K, ck_fp4_format format, int n_experts);
+
+/*
+ * Quantize, per block with absmax a:
+ *   CK_MXFP4  scale = 2^(floor(log2 a) - 2), exponent clamped to [-127, 127]; code = e2m1(x / scale)
+ *   CK_NVFP4  scale = e4m3(a / fl(6 t)); code = e2m1(x / fl(scale * t)), 0 where that divisor is 0
+ * e2m1() and e4m3() round the exact quotient half to even and saturate (6 and 448); fl() rounds to
+ * fp32.  A block that holds a NaN or an infinity gets a NaN scale and zero codes, and so does every
+ * block where t is not a positive finite number.
+ *
+ *   x, x_dtype, M, K, stride_m, stride_k
+ *                 as in ck_rotate_quant; K a positive multiple of the block
+ *   tensor_scale  device pointer to t, or NULL for 1 (NULL for CK_MXFP4)
+ *   offsets       NULL: one matrix.  Otherwise n_experts + 1 (n_experts 1 to 1024) device int32:
+ *                 expert e's rows are [offsets[e], offsets[e + 1]).  They must not decrease; they
+ *                 are clamped to [0, M], and a decreasing pair is an empty expert.  Rows of no
+ *                 expert are neither read nor written.
+ *   codes         (M, K / 2) bytes, row pitch ldq >= K / 2
+ *   scales        ck_fp4_scales_bytes(M, K, format, offsets ? n_experts : 0) bytes; the bytes of a
+ *                 written tile past the last row and block are 0, tiles of no expert are not written
+ * Errors: CK_ERR_INVALID_ARG, CK_ERR_UNSUPPORTED (M or K of 2^31 or more, or more than 2^31 - 1
+ * tiles of 128 x 256), CK_ERR_CUDA.
+ */
+ck_status ck_quant_fp4(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, int64_t stride_m,
+                       int64_t stride_k, ck_fp4_format format, const float* tensor_scale,
+                       const int32_t* offsets, int n_experts, uint8_t* codes, int64_t ldq,
+                       uint8_t* scales, cudaStream_t stream);
+
+/* The values back: out[m, k] = cvt(fl(code * scale * t)), (M, K) of out_dtype (CK_F32/F16/BF16), row
+ * pitch ldo >= K.  Other arguments and errors as ck_quant_fp4. */
+ck_status ck_dequant_fp4(const uint8_t* codes, int64_t ldq, const uint8_t* scales, int64_t M, int64_t K,
+                         ck_fp4_format format, const float* tensor_scale, const int32_t* offsets,
+                         int n_experts, void* out, ck_dtype out_dtype, int64_t ldo,
+                         cudaStream_t stream);
+
+/*
+ * The linear on microscaled fp4: out[m, n] = cvt(fl(acc * fl(tx * tw)) + bias[n]), acc the fp32
+ * tensor-core sum over k of the fp4 values of x and w without their tensor scales tx and tw.
+ *
+ *   x, x_dtype, M, K, stride_m, stride_k
+ *             CK_F32/CK_F16/CK_BF16: quantized first as by ck_quant_fp4 with x_tensor_scale.
+ *             CK_FP4: x holds (M, K / 2) codes with row pitch stride_m (a multiple of 16 bytes, x
+ *             16-byte aligned; stride_k must be 1) and x_scales their scale tiles.
+ *   x_tensor_scale, w_tensor_scale
+ *             device pointers to tx and tw, or NULL for 1 (NULL for CK_MXFP4)
+ *   w         (N, K / 2) codes, row pitch w_ld: a multiple of 16 bytes, w 16-byte aligned
+ *   w_scales  the weight's scale tiles, ck_fp4_scales_bytes(N, K, format, 0) bytes
+ *   bias      (N,) of bias_dtype, or NULL
+ *   out       (M, N) of out_dtype, row pitch ldo >= N
+ *   workspace, workspace_bytes
+ *             for floating-point x: at least ck_fp4_linear_workspace_bytes(M, K, format, 0) bytes of
+ *             device scratch, 256-byte aligned: the codes (row pitch K / 2 rounded up to 16), then,
+ *             256-byte aligned, the scale tiles.  Not used for CK_FP4.
+ * Errors: CK_ERR_INVALID_ARG, CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (a size of 2^31 or more, or as
+ * many tiles), CK_ERR_CUDA.
+ */
+ck_status ck_fp4_linear(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, int64_t stride_m,
+                        int64_t stride_k, ck_fp4_format format, const uint8_t* x_scales,
+                        const float* x_tensor_scale, const uint8_t* w, int64_t N, int64_t w_ld,
+                        const uint8_t* w_scales, const float* w_tensor_scale, const void* bias,
+                        ck_dtype bias_dtype, void* out, ck_dtype out_dtype, int64_t ldo,
+                        void* workspace, size_t workspace_bytes, int* dev_status,
+                        cudaStream_t stream);
+size_t ck_fp4_linear_workspace_bytes(int64_t M, int64_t K, ck_fp4_format format, int n_experts);
+
+/*
+ * ck_fp4_linear with the rows sorted by expert and one weight matrix per expert (a mixture of
+ * experts' layer after its router): rows [offsets[e], offsets[e + 1]) of x times expert e's weight.
+ * The offsets stay on the device: nothing is read back, and a captured call follows them.  Rows of
+ * no expert (before offsets[0], from offsets[n_experts] on) are left as they were in out.
+ *
+ *   offsets, n_experts  as in ck_quant_fp4 (not NULL)
+ *   x_scales            for CK_FP4 x: the scale tiles of rows sorted by the same offsets
+ *   w                   expert e's (N, K / 2) codes at w + e * w_stride bytes; w_stride a multiple
+ *                       of 16, at least N * w_ld
+ *   w_scales            the experts' scale tiles one after the other, ck_fp4_scales_bytes(N, K,
+ *                       format, 0) bytes each
+ *   w_tensor_scale      (n_experts,) fp32, or NULL for 1
+ *   bias                (n_experts, N) contiguous, or NULL
+ *   workspace           ck_fp4_linear_workspace_bytes(M, K, format, n_experts) bytes
+ * Everything else and the errors as ck_fp4_linear.
+ */
+ck_status ck_fp4_expert_linear(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, int64_t stride_m,
+                               int64_t stride_k, ck_fp4_format format, const uint8_t* x_scales,
+                               const float* x_tensor_scale, const int32_t* offsets, int n_experts,
+                               const uint8_t* w, int64_t N, int64_t w_ld, int64_t w_stride,
+                               const uint8_t* w_scales, const float* w_tensor_scale, const void* bias,
+                               ck_dtype bias_dtype, void* out, ck_dtype out_dtype, int64_t ldo,
+                               void* workspace, size_t workspace_bytes, int* dev_status,
+                               cudaStream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* ck_status_string(ck_status status);

@@ -17,7 +17,9 @@ LIB_PATH = os.path.join(_HERE, "libck.so")
 
 CK_OK, CK_ERR_INVALID_ARG, CK_ERR_UNSUPPORTED, CK_ERR_OVERFLOW = 0, 1, 2, 3
 CK_ERR_WORKSPACE, CK_ERR_CUDA, CK_ERR_TIMEOUT = 4, 5, 6
-CK_F32, CK_F16, CK_BF16, CK_I8 = 0, 1, 2, 3
+CK_F32, CK_F16, CK_BF16, CK_I8, CK_FP4 = 0, 1, 2, 3, 4
+CK_MXFP4, CK_NVFP4 = 0, 1
+FP4_BLOCK = {CK_MXFP4: 32, CK_NVFP4: 16}
 
 DTYPE_CODE = {torch.float32: CK_F32, torch.float16: CK_F16, torch.bfloat16: CK_BF16,
               torch.int8: CK_I8}
@@ -44,6 +46,14 @@ SIGNATURES = {
     "ck_w8a8_linear_workspace_bytes": ([_I64, _I64, _I64, _I64], _SZ),
     "ck_rotate_quant_packed": ([_P, _I, _I64, _I64, _I64, _I64, _P, _I, _P, _I, ctypes.c_uint64,
                                 ctypes.c_uint64, _P, _I64, _P, _P], _I),
+    "ck_fp4_scales_bytes": ([_I64, _I64, _I, _I], _SZ),
+    "ck_fp4_linear_workspace_bytes": ([_I64, _I64, _I, _I], _SZ),
+    "ck_quant_fp4": ([_P, _I, _I64, _I64, _I64, _I64, _I, _P, _P, _I, _P, _I64, _P, _P], _I),
+    "ck_dequant_fp4": ([_P, _I64, _P, _I64, _I64, _I, _P, _P, _I, _P, _I, _I64, _P], _I),
+    "ck_fp4_linear": ([_P, _I, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _I64, _I64, _P, _P, _P, _I,
+                       _P, _I, _I64, _P, _SZ, _P, _P], _I),
+    "ck_fp4_expert_linear": ([_P, _I, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _I, _P, _I64, _I64,
+                              _I64, _P, _P, _P, _I, _P, _I, _I64, _P, _SZ, _P, _P], _I),
     "ck_status_string": ([_I], ctypes.c_char_p),
 }
 
@@ -386,3 +396,204 @@ def ck_unpack_w4(packed: torch.Tensor, K: int, out: torch.Tensor | None = None,
                                 _stream(stream))
     _check(st, "ck_unpack_w4")
     return out
+
+
+# ------------------------------------------------------------------ microscaled fp4
+
+def fp4_scales_bytes(M: int, K: int, fmt: int, n_experts: int = 0) -> int:
+    return int(lib().ck_fp4_scales_bytes(M, K, fmt, n_experts))
+
+
+def fp4_workspace_bytes(M: int, K: int, fmt: int, n_experts: int = 0) -> int:
+    return int(lib().ck_fp4_linear_workspace_bytes(M, K, fmt, n_experts))
+
+
+def _check_fp4(fmt: int, K: int):
+    if fmt not in FP4_BLOCK:
+        raise ValueError(f"fmt must be CK_MXFP4 or CK_NVFP4, got {fmt!r}")
+    if K <= 0 or K % FP4_BLOCK[fmt]:
+        raise ValueError(f"K = {K} must be a positive multiple of the block, {FP4_BLOCK[fmt]}")
+
+
+def _check_codes(t: torch.Tensor, what: str, shape: tuple):
+    if t.dtype != torch.uint8 or tuple(t.shape) != shape or t.stride(-1) != 1:
+        raise ValueError(f"{what} must be a uint8 {shape} view with unit inner stride; got "
+                         f"{tuple(t.shape)} {t.dtype} strides {t.stride()}")
+
+
+def _check_scales(t: torch.Tensor, what: str, nbytes: int):
+    if t.dtype != torch.uint8 or t.numel() < nbytes or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous uint8 tensor of at least {nbytes} bytes; got "
+                         f"{t.numel()} of {t.dtype}")
+
+
+def _check_tensor_scale(t: torch.Tensor | None, what: str, n: int, fmt: int):
+    if t is None:
+        return
+    if fmt == CK_MXFP4:
+        raise ValueError(f"{what}: CK_MXFP4 has no tensor scale")
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous fp32 tensor of {n} values; got {t.numel()} of "
+                         f"{t.dtype}")
+
+
+def _check_offsets(offsets: torch.Tensor | None) -> int:
+    """Number of experts (0 without offsets)."""
+    if offsets is None:
+        return 0
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or \
+            offsets.numel() < 2:
+        raise ValueError("offsets must be a contiguous 1-D int32 tensor of one more value than "
+                         f"experts; got {tuple(offsets.shape)} {offsets.dtype}")
+    return offsets.numel() - 1
+
+
+def _float_code(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError(f"{what} must be fp32, fp16 or bf16; got {t.dtype}")
+    return DTYPE_CODE[t.dtype]
+
+
+def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None = None,
+                 offsets: torch.Tensor | None = None, codes: torch.Tensor | None = None,
+                 scales: torch.Tensor | None = None, stream=None):
+    """A 2-D (M, K) view to microscaled fp4 (fmt CK_MXFP4 or CK_NVFP4); returns (codes uint8
+    (M, K/2) with rows at a pitch of 16 bytes, scales uint8 in tiles).  offsets (n_experts + 1 int32
+    on the device): rows sorted by expert, each expert's scales in tiles of its own."""
+    M, K = x.shape
+    _check_fp4(fmt, K)
+    dt = _float_code(x, "x")
+    _same_device(x, tensor_scale, offsets, codes, scales)
+    _check_tensor_scale(tensor_scale, "tensor_scale", 1, fmt)
+    E = _check_offsets(offsets)
+    nbytes = fp4_scales_bytes(M, K, fmt, E)
+    if codes is None:
+        codes = torch.empty(M, (K // 2 + 15) // 16 * 16, dtype=torch.uint8,
+                            device=x.device)[:, : K // 2]
+    if scales is None:
+        scales = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    _check_codes(codes, "codes", (M, K // 2))
+    _check_scales(scales, "scales", nbytes)
+    with torch.cuda.device(x.device):
+        st = lib().ck_quant_fp4(_ptr(x), dt, M, K, x.stride(0), x.stride(1), fmt, _ptr(tensor_scale),
+                                _ptr(offsets), E, _ptr(codes), max(codes.stride(0), K // 2),
+                                _ptr(scales), _stream(stream))
+    _check(st, "ck_quant_fp4")
+    return codes, scales
+
+
+def ck_dequant_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: int, *,
+                   tensor_scale: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                   stream=None) -> torch.Tensor:
+    """The values that codes (M, K/2) and their scale tiles stand for, (M, K)."""
+    M, K = codes.shape[0], 2 * codes.shape[1]
+    _check_fp4(fmt, K)
+    _check_codes(codes, "codes", (M, K // 2))
+    _same_device(codes, scales, tensor_scale, offsets)
+    _check_tensor_scale(tensor_scale, "tensor_scale", 1, fmt)
+    E = _check_offsets(offsets)
+    _check_scales(scales, "scales", fp4_scales_bytes(M, K, fmt, E))
+    if out is None:
+        out = torch.empty(M, K, dtype=out_dtype, device=codes.device)
+    _check_out(out, M, K, codes)
+    odt = _float_code(out, "out")
+    with torch.cuda.device(codes.device):
+        st = lib().ck_dequant_fp4(_ptr(codes), max(codes.stride(0), K // 2), _ptr(scales), M, K, fmt,
+                                  _ptr(tensor_scale), _ptr(offsets), E, _ptr(out), odt,
+                                  max(out.stride(0), K), _stream(stream))
+    _check(st, "ck_dequant_fp4")
+    return out
+
+
+def _fp4_product(where: str, x, offsets, w, w_scales, fmt, bias, x_scales, x_tensor_scale,
+                 w_tensor_scale, out, out_dtype, workspace, dev_status, stream):
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be 2-D and the weights (N, K/2), or (n_experts, N, K/2)")
+    E, N = w.shape[0], w.shape[1]
+    codes_in = x.dtype == torch.uint8
+    M, K = x.shape[0], x.shape[1] * 2 if codes_in else x.shape[1]
+    _check_fp4(fmt, K)
+    _same_device(x, offsets, w, w_scales, bias, x_scales, x_tensor_scale, w_tensor_scale, workspace,
+                 dev_status)
+    _check_codes(w, "w_codes", (E, N, K // 2))
+    per = fp4_scales_bytes(N, K, fmt)
+    _check_scales(w_scales, "w_scales", E * per)
+    if offsets is not None and (w_scales.dim() != 2 or tuple(w_scales.shape) != (E, per)):
+        raise ValueError(f"w_scales must be (n_experts, {per}); got {tuple(w_scales.shape)}")
+    _check_tensor_scale(x_tensor_scale, "x_tensor_scale", 1, fmt)
+    _check_tensor_scale(w_tensor_scale, "w_tensor_scale", E, fmt)
+    if offsets is not None and _check_offsets(offsets) != E:
+        raise ValueError(f"offsets must hold {E + 1} values for {E} experts; got {offsets.numel()}")
+    bdt = CK_F32
+    if bias is not None:
+        bdt = _float_code(bias, "bias")
+        if bias.numel() != E * N or not bias.is_contiguous():
+            raise ValueError(f"bias must hold {E} x {N} contiguous values; got {tuple(bias.shape)}")
+    nE = 0 if offsets is None else E
+    if codes_in:
+        _check_codes(x, "x", (M, K // 2))
+        if x_scales is None:
+            raise ValueError("x holds fp4 codes: x_scales must be given")
+        _check_scales(x_scales, "x_scales", fp4_scales_bytes(M, K, fmt, nE))
+        dt = CK_FP4
+    else:
+        dt = _float_code(x, "x")
+    if out is None:
+        if codes_in and out_dtype is None:
+            out_dtype = bias.dtype if bias is not None else torch.bfloat16
+        out = torch.empty(M, N, dtype=out_dtype or x.dtype, device=x.device)
+    _check_out(out, M, N, x)
+    odt = _float_code(out, "out")
+    with torch.cuda.device(x.device):
+        if workspace is None and not codes_in:
+            workspace = torch.empty(max(fp4_workspace_bytes(M, K, fmt, nE), 1), dtype=torch.uint8,
+                                    device=x.device)
+        wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        sm = max(x.stride(0), K // 2) if codes_in else x.stride(0)
+        ldo = max(out.stride(0), N)
+        if offsets is None:
+            st = lib().ck_fp4_linear(
+                _ptr(x), dt, M, K, sm, x.stride(1), fmt, _ptr(x_scales), _ptr(x_tensor_scale), _ptr(w),
+                N, w.stride(1), _ptr(w_scales), _ptr(w_tensor_scale), _ptr(bias), bdt, _ptr(out), odt,
+                ldo, _ptr(workspace), wsb, _ptr(dev_status), _stream(stream))
+        else:
+            st = lib().ck_fp4_expert_linear(
+                _ptr(x), dt, M, K, sm, x.stride(1), fmt, _ptr(x_scales), _ptr(x_tensor_scale),
+                _ptr(offsets), E, _ptr(w), N, w.stride(1), w.stride(0), _ptr(w_scales),
+                _ptr(w_tensor_scale), _ptr(bias), bdt, _ptr(out), odt, ldo, _ptr(workspace), wsb,
+                _ptr(dev_status), _stream(stream))
+    _check(st, where)
+    return out
+
+
+def ck_fp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, fmt: int,
+                  bias: torch.Tensor | None = None, *, x_scales: torch.Tensor | None = None,
+                  x_tensor_scale: torch.Tensor | None = None,
+                  w_tensor_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
+                  dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The linear on microscaled fp4: x (M, K) activations (quantized on the way), or uint8 codes
+    (M, K/2) with x_scales; w_codes (N, K/2) and w_scales as ck_quant_fp4 returns them.  Returns
+    out (M, N)."""
+    if w_codes.dim() != 2:
+        raise ValueError(f"w_codes must be (N, K/2); got {tuple(w_codes.shape)}")
+    return _fp4_product("ck_fp4_linear", x, None, w_codes.unsqueeze(0), w_scales, fmt, bias, x_scales,
+                        x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status, stream)
+
+
+def ck_fp4_expert_linear(x: torch.Tensor, offsets: torch.Tensor, w_codes: torch.Tensor,
+                         w_scales: torch.Tensor, fmt: int, bias: torch.Tensor | None = None, *,
+                         x_scales: torch.Tensor | None = None,
+                         x_tensor_scale: torch.Tensor | None = None,
+                         w_tensor_scale: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                         workspace: torch.Tensor | None = None,
+                         dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """ck_fp4_linear with rows sorted by expert: rows [offsets[e], offsets[e+1]) of x times
+    w_codes[e] (n_experts, N, K/2) with w_scales[e] (n_experts, bytes), w_tensor_scale[e] and
+    bias[e].  offsets stays on the device; rows of no expert keep what `out` held."""
+    if offsets is None:
+        raise ValueError("offsets must be given")
+    return _fp4_product("ck_fp4_expert_linear", x, offsets, w_codes, w_scales, fmt, bias, x_scales,
+                        x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status, stream)

@@ -1,0 +1,591 @@
+// ck_fp4_gemm.cu -- the product of microscaled fp4 activations and weights:
+//   out[m, n] = cvt(fl(acc[m, n] * alpha) + bias[n]),   alpha = x_tensor_scale * w_tensor_scale
+//   acc[m, n] = sum over blocks of sx[m, block] * sw[n, block] * (sum over the block of x * w)
+// for one weight matrix, or with the rows sorted by expert and a matrix per expert.
+//
+// Bound: 2 M N K operations on the tensor cores (tcgen05.mma kind::mxf4nvf4, which multiplies the
+// block scales in) when there are many rows, the weights' bytes from HBM when there are few.
+//
+// Persistent; a tile is 128 channels per CTA times BN rows, transposed (D[n, m], channels on the
+// tensor-memory lanes), so that a tile of few rows, an expert's, wastes columns of the MMA and not
+// its 128 lanes.  CG = 2: two CTAs of a cluster form one 256 x BN tile with
+// tcgen05.mma.cta_group::2; each holds its own 128 channels and half of the rows' codes, so a
+// byte of shared memory feeds twice the math.  Per stage of 256 k (four MMAs):
+//   warp 0   TMA of the weights' and rows' codes (128-byte rows, 128-byte swizzle) and of their
+//            scale tiles; the weights' part of the first stages before the wait for the kernel
+//            before this one (the quantizer)
+//   warp 1   copies the scale tiles from shared to tensor memory (tcgen05.cp, in order with the
+//            MMAs that read them) and issues the MMAs: the CTA of rank 0 for both CTAs.  The other
+//            CTA's warp 1 forwards "stage full" to rank 0 instead.
+//   warps 4-11  the epilogue: two warps per lane quarter on alternate 16-row chunks, from one of
+//            two accumulators while the MMAs fill the other; outputs transposed through a staging
+//            buffer into 16-byte stores
+// Every wait is bounded; a CTA leaves only after its own copies have landed, the MMAs that read
+// its memory have completed and the arrivals that were sent to it have come.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "ck_device.cuh"
+#include "ck_fp4.cuh"
+#include "ck_fp4_mma.cuh"
+#include "ck_gemm_common.cuh"
+#include "ck_internal.h"
+
+namespace ck {
+
+namespace fp4g {
+constexpr int BW = 128;                 // channels per CTA
+constexpr int BK = 256;                 // k per stage: 128 bytes of codes
+constexpr int BN_MAX = 192;
+constexpr int WARP_TMA = 0, WARP_MMA = 1, EPI_WARP0 = 4, EPI_WARPS = 8;
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int STAGES_MAX = 8;
+constexpr uint32_t A_BYTES = BW * BK / 2;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t SF_COL = 2 * BN_MAX;   // two accumulators, then two sets of scale columns
+constexpr uint32_t SF_SET = 48;
+constexpr int EPI_STAGE_BYTES = 16 * 32 * 4;
+constexpr size_t SMEM_MAX = 227 * 1024 - 1024;   // less the static shared memory
+static_assert(SF_COL + 2 * SF_SET <= TMEM_COLS, "accumulators and scales fit");
+}  // namespace fp4g
+
+struct Fp4GemmParams {
+    int64_t M, N;
+    int num_kb;           // stages per tile: ceil(K / 256)
+    int k64;              // MMA steps per tile: ceil(K / 64)
+    int BN;               // rows per tile
+    int nblk;             // 128-row scale blocks a tile's rows may touch
+    int tiles_n;          // tiles along the channels
+    int stages;
+    uint32_t b_bytes;     // a CTA's codes of the rows per stage
+    uint32_t sfa_bytes, sfb_bytes, stage_bytes;
+    uint32_t idesc;
+    int n_experts;        // 1 without offsets
+    int n_sf_blocks;      // scale blocks of one weight matrix
+    const int32_t* offsets;
+    const float* x_ts;
+    const float* w_ts;    // one per expert
+    const void* bias;     // (n_experts, N)
+    ck_dtype bias_dt;
+    void* out;
+    int64_t ldo;
+    int* dev_status;
+};
+
+__device__ __forceinline__ float load_any(const void* p, ck_dtype dt, int64_t i) {
+    if (dt == CK_F32) return load_scale<float>(p, i);
+    if (dt == CK_F16) return load_scale<__half>(p, i);
+    return load_scale<__nv_bfloat16>(p, i);
+}
+
+// One tile: expert, first row, rows, first channel of the CTA's 128, and where its rows' scales are.
+struct Fp4Tile {
+    int e;
+    int64_t m0;        // first row
+    int rows;          // rows of the expert from m0 on, at most BN
+    int64_t n0;        // first channel of the tile
+    int sf_block;      // 128-row scale block of m0
+    int sf_shift;      // 32-row groups of that block before m0
+};
+
+template <int CG>
+__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4GemmParams& p, const int* cum, int t) {
+    // the last expert whose first tile is not after t
+    int lo = 0, hi = p.n_experts - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    Fp4Tile r;
+    r.e = lo;
+    int64_t first = 0, last = p.M, block = 0;
+    if (p.offsets) {
+        const RowRange rr = expert_rows(p.offsets, lo, p.M);
+        first = rr.lo;
+        last = rr.hi;
+        block = expert_scale_block(first, lo);
+    }
+    const int u = t - cum[lo];
+    const int i = u / p.tiles_n;
+    const int64_t off = (int64_t)i * p.BN;
+    r.n0 = (int64_t)(u % p.tiles_n) * (fp4g::BW * CG);
+    r.m0 = first + off;
+    const int64_t left = last - r.m0;
+    r.rows = (int)(left < p.BN ? left : p.BN);
+    r.sf_block = (int)(block + off / kFp4TileRows);
+    r.sf_shift = (int)(off % kFp4TileRows) / 32;
+    return r;
+}
+
+template <typename OutT, bool NV, int CG>
+__global__ void __launch_bounds__(fp4g::THREADS, 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap xmap,
+                    const __grid_constant__ CUtensorMap wmap,
+                    const __grid_constant__ CUtensorMap xsmap,
+                    const __grid_constant__ CUtensorMap wsmap, Fp4GemmParams p) {
+    using namespace fp4g;
+    constexpr int SF_TILES = NV ? 4 : 2;     // scale tiles per stage and 128 rows
+    extern __shared__ __align__(1024) unsigned char fp4_smem[];
+    unsigned char* ring = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(fp4_smem) + 1023) & ~uintptr_t(1023));
+    const uint32_t S = (uint32_t)p.stages;
+    unsigned char* epi_stage = ring + (size_t)S * p.stage_bytes;
+    int* cum = reinterpret_cast<int*>(epi_stage + EPI_WARPS * EPI_STAGE_BYTES);   // [n_experts + 1]
+
+    __shared__ __align__(8) uint64_t full[STAGES_MAX], peer_full[STAGES_MAX], empty[STAGES_MAX];
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain_bar;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_flag;
+    __shared__ uint32_t commits[2];          // rank 0's count of stage and of accumulator commits
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+    const int unit = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES_MAX; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&peer_full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], EPI_WARPS * CG);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_flag = 0;
+        commits[0] = commits[1] = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&xmap);
+        tma_prefetch_desc(&wmap);
+        tma_prefetch_desc(&xsmap);
+        tma_prefetch_desc(&wsmap);
+    }
+    if (warp == WARP_MMA) {
+        tmem_alloc_cg<CG>(&tmem_base_sh, TMEM_COLS);
+        tmem_relinquish_cg<CG>();
+    }
+    // tiles before each expert's: a running sum over the experts, 32 at a time
+    if (warp == 2) {
+        int before = 0;
+        for (int e0 = 0; e0 < p.n_experts; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < p.n_experts) {
+                int64_t m = p.M;
+                if (p.offsets) {
+                    const RowRange r = expert_rows(p.offsets, e, p.M);
+                    m = r.hi - r.lo;
+                }
+                n = (int)((m + p.BN - 1) / p.BN) * p.tiles_n;
+            }
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            if (e < p.n_experts) cum[e] = before + sum - n;
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) cum[p.n_experts] = before;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();   // the peer's barriers are ready for arrivals
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_base_sh;
+    const int tiles = cum[p.n_experts];
+    const uint32_t num_kb = (uint32_t)p.num_kb;
+    const uint32_t my_tiles = tiles > unit ? (uint32_t)((tiles - unit + units - 1) / units) : 0u;
+    const uint32_t my_stages = my_tiles * num_kb;
+
+    if (warp == WARP_TMA) {
+        // ---------------------------------------------------------------- loads
+        if (lane == 0) {
+            uint32_t issued = 0;
+            bool ok = true;
+            auto load_w = [&](const Fp4Tile& t, uint32_t kb, uint32_t s) {
+                unsigned char* st = ring + (size_t)s * p.stage_bytes;
+                mbar_arrive_expect_tx(&full[s], A_BYTES + p.b_bytes + p.sfa_bytes + p.sfb_bytes);
+                tma_load_3d(st, &wmap, &full[s], (int32_t)(kb * (BK / 2)),
+                            (int32_t)t.n0 + (int32_t)rank * BW, t.e);
+                tma_load_3d(st + A_BYTES + p.b_bytes, &wsmap, &full[s], 0, (int32_t)(kb * SF_TILES),
+                            t.e * p.n_sf_blocks + (int)(t.n0 / BW) + (int)rank);
+            };
+            auto load_x = [&](const Fp4Tile& t, uint32_t kb, uint32_t s) {
+                unsigned char* st = ring + (size_t)s * p.stage_bytes;
+                tma_load_2d(st + A_BYTES, &xmap, &full[s], (int32_t)(kb * (BK / 2)),
+                            (int32_t)t.m0 + (int32_t)rank * (p.BN / CG));
+                tma_load_3d(st + A_BYTES + p.b_bytes + p.sfa_bytes, &xsmap, &full[s], 0,
+                            (int32_t)(kb * SF_TILES), t.sf_block);
+            };
+            // the weights of the first stages, then the rows once the kernel before has written them
+            const uint32_t head = my_stages < S ? my_stages : S;
+            Fp4Tile t = {};
+            uint32_t kb = 0, lt = 0;
+            for (uint32_t i = 0; i < head; ++i) {
+                if (kb == 0) t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
+                load_w(t, kb, i);
+                if (++kb == num_kb) {
+                    kb = 0;
+                    ++lt;
+                }
+            }
+            grid_dependency_wait();
+            kb = lt = 0;
+            uint32_t s = 0, phase = 0;
+            for (uint32_t i = 0; i < my_stages; ++i) {
+                if (kb == 0) t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
+                if (i >= head) {
+                    if (!mbar_wait_cluster(&empty[s], phase ^ 1u, &abort_flag, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    load_w(t, kb, s);
+                }
+                load_x(t, kb, s);
+                ++issued;
+                if (++kb == num_kb) {
+                    kb = 0;
+                    ++lt;
+                }
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok)   // copies in flight land before the CTA leaves
+                for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
+                    mbar_wait(&full[j % S], (j / S) & 1u, nullptr, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == WARP_MMA && rank == 0) {
+        // ---------------------------------------------------------------- MMA issuer
+        // the whole warp takes every wait and computes every operand; one elected lane issues
+        grid_dependency_wait();
+        const bool leader = elect_one();
+        const uint32_t ring_u = smem_u32(ring);
+        uint32_t s = 0, phase = 0, n_stage = 0, n_acc = 0;
+        bool ok = true;
+        for (uint32_t lt = 0; ok && lt < my_tiles; ++lt) {
+            const Fp4Tile t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
+            const uint32_t acc = lt & 1u;
+            if (lt >= 2 && !__all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], ((lt >> 1) - 1) & 1u,
+                                                                      &abort_flag, p.dev_status)))
+                break;
+            tc_fence_after();
+            const uint32_t d = tmem_base + acc * BN_MAX;
+            for (uint32_t kb = 0; kb < num_kb; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, &abort_flag, p.dev_status)) ||
+                    (CG == 2 && !__all_sync(0xffffffffu, mbar_wait_cluster(&peer_full[s], phase, &abort_flag,
+                                                                           p.dev_status)))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t st = ring_u + s * p.stage_bytes;
+                const uint32_t sfa = tmem_base + SF_COL + (n_stage & 1u) * SF_SET;
+                const uint32_t sfb = sfa + 16;
+                const uint32_t left = (uint32_t)p.k64 - kb * 4;
+                const uint32_t steps = left < 4 ? left : 4;
+                if (leader) {
+                    const uint64_t sa = smem_desc_scales(st + A_BYTES + p.b_bytes);
+                    const uint64_t sb = smem_desc_scales(st + A_BYTES + p.b_bytes + p.sfa_bytes);
+#pragma unroll
+                    for (int j = 0; j < SF_TILES; ++j) {
+                        tc_cp_scales<CG>(sfa + 4 * j, sa + (uint64_t)(j * (kFp4TileBytes >> 4)));
+                        tc_cp_scales<CG>(sfb + 4 * j * p.nblk, sb + (uint64_t)(j * (kFp4TileBytes >> 4)));
+                        if (p.nblk == 2)
+                            tc_cp_scales<CG>(sfb + 8 * j + 4,
+                                             sb + (uint64_t)((SF_TILES + j) * (kFp4TileBytes >> 4)));
+                    }
+                    const uint64_t ad = smem_desc_k_sw128(st), bd = smem_desc_k_sw128(st + A_BYTES);
+                    for (uint32_t j = 0; j < steps; ++j) {
+                        // MX: a tile holds the scales of two steps, bytes 0-1 and 2-3 of a word
+                        const uint32_t tile = NV ? j : j >> 1, half = NV ? 0u : (j & 1u) * 2u;
+                        tc_mma_fp4<NV, CG>(d, ad + (uint64_t)(j * 2), bd + (uint64_t)(j * 2),
+                                           p.idesc | (half << 4) | (half << 29), sfa + 4 * tile,
+                                           sfb + 4 * tile * p.nblk + t.sf_shift, (kb | j) != 0 ? 1u : 0u);
+                    }
+                    tc_commit_cg<CG>(&empty[s]);
+                    if (kb + 1 == num_kb) tc_commit_cg<CG>(&acc_full[acc]);
+                }
+                __syncwarp();
+                ++n_stage;
+                if (kb + 1 == num_kb) ++n_acc;
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // every MMA and copy issued above has completed once drain_bar flips
+        if (leader) {
+            tc_commit_local<CG>(&drain_bar);
+            mbar_wait(&drain_bar, 0, nullptr, p.dev_status);
+            commits[0] = n_stage;
+            commits[1] = n_acc;
+        }
+        __syncwarp();
+    } else if (CG == 2 && warp == WARP_MMA) {
+        // ---------------------------------------------------------------- forward "full" to rank 0
+        grid_dependency_wait();
+        uint32_t s = 0, phase = 0;
+        for (uint32_t i = 0; i < my_stages; ++i) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, &abort_flag, p.dev_status))) break;
+            if (lane == 0) mbar_arrive_remote(&peer_full[s], 0);
+            if (++s == S) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
+        __syncwarp();
+    } else if (warp >= EPI_WARP0) {
+        // ---------------------------------------------------------------- epilogue
+        const int q = warp & 3;                        // TMEM lanes 32q .. 32q + 31
+        const int eh = (warp - EPI_WARP0) >> 2;        // 16-row chunks eh, eh + 2, ...
+        grid_dependency_wait();
+        const float xts = p.x_ts ? __ldg(p.x_ts) : 1.0f;
+        for (uint32_t lt = 0; lt < my_tiles; ++lt) {
+            const Fp4Tile t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
+            const uint32_t acc = lt & 1u;
+            const int64_t n = t.n0 + (int64_t)rank * BW + q * 32 + lane;
+            const bool n_ok = n < p.N;
+            const float alpha = __fmul_rn(xts, p.w_ts ? __ldg(p.w_ts + t.e) : 1.0f);
+            const float bs = p.bias && n_ok ? load_any(p.bias, p.bias_dt, (int64_t)t.e * p.N + n) : 0.0f;
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[acc], (lt >> 1) & 1u, &abort_flag,
+                                                           p.dev_status)))
+                break;
+            tc_fence_after();
+            const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN_MAX;
+            OutT* obase = static_cast<OutT*>(p.out) + (n - lane);   // the warp's first channel
+            constexpr int PER16 = 16 / (int)sizeof(OutT);
+            const bool vec = n - lane + 32 <= p.N && reinterpret_cast<uintptr_t>(obase) % 16 == 0 &&
+                             p.ldo % PER16 == 0;
+            OutT* stage = reinterpret_cast<OutT*>(epi_stage + (size_t)(warp - EPI_WARP0) * EPI_STAGE_BYTES);
+            for (int c0 = 16 * eh; c0 < t.rows; c0 += 32) {
+                uint32_t r[16];
+                tc_ld_32x32b_x16(tacc + (uint32_t)c0, r);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float o = __fmul_rn(__uint_as_float(r[j]), alpha);
+                    if (p.bias) o = __fadd_rn(o, bs);
+                    if (vec) OutStore<OutT>::one(stage + j * 32 + lane, o);
+                    else if (c0 + j < t.rows && n_ok)
+                        OutStore<OutT>::one(obase + lane + (t.m0 + c0 + j) * p.ldo, o);
+                }
+                if (vec) {
+                    __syncwarp();
+                    constexpr int PIECES = 32 / PER16;
+#pragma unroll
+                    for (int i = lane; i < 16 * PIECES; i += 32) {
+                        const int row = i / PIECES, pc = i % PIECES;
+                        if (c0 + row < t.rows)
+                            *reinterpret_cast<uint4*>(obase + (t.m0 + c0 + row) * p.ldo + pc * PER16) =
+                                *reinterpret_cast<const uint4*>(stage + row * 32 + pc * PER16);
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2 && rank != 0) mbar_arrive_remote(&acc_empty[acc], 0);
+                else mbar_arrive(&acc_empty[acc]);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) {
+        // rank 0's MMAs have completed (its drain) and its counts are readable: wait for the
+        // arrivals of its commits at this CTA's barriers, then for the peer to have done the same
+        cluster_sync_all();
+        if (tid == 0) {
+            const uint32_t n = dsmem_load_u32(&commits[0], 0), a = dsmem_load_u32(&commits[1], 0);
+            for (uint32_t j = n > S ? n - S : 0; j < n; ++j)
+                mbar_wait_cluster(&empty[j % S], (j / S) & 1u, nullptr, nullptr);
+            for (uint32_t j = a > 2 ? a - 2 : 0; j < a; ++j)
+                mbar_wait_cluster(&acc_full[j & 1u], (j >> 1) & 1u, nullptr, nullptr);
+        }
+        __syncthreads();
+        cluster_sync_all();
+    }
+    if (warp == WARP_MMA) {
+        tc_fence_after();
+        tmem_dealloc_cg<CG>(tmem_base, TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+struct Fp4Shape {
+    int cg, bn;
+};
+
+// CTAs per tile and rows per tile, by the estimated time of the busiest unit: waves of tiles, each
+// the larger of its MMA time (BN / 2 cycles per 64 k: both SMs of a pair at 16384 multiply-adds a
+// cycle each; BN for... one SM has half the pair's rate on half the channels, the same time) and the
+// time its bytes take to arrive at about 64 bytes a cycle and SM, plus a fixed cost.
+static Fp4Shape choose_shape(int64_t M, int64_t N, int64_t num_kb, int n_experts, int sms) {
+    // 64-row steps keep a tile's first scale column even; 32 rows only where one tile holds them all
+    static const Fp4Shape all[] = {{2, 192}, {2, 128}, {1, 128}, {1, 64}, {1, 32}};
+    const int64_t m = (M + n_experts - 1) / n_experts;   // rows of an expert, were they even
+    Fp4Shape best = all[0];
+    double best_cost = -1.0;
+    for (const Fp4Shape& s : all) {
+        if (s.bn == 32 && M > 32) continue;
+        const int64_t units = sms / s.cg;
+        const int64_t tiles = (int64_t)n_experts * ((m + s.bn - 1) / s.bn) *
+                              ((N + 128 * s.cg - 1) / (128 * s.cg));
+        const double mma = 4.0 * s.bn / 2;
+        const double load = (128.0 * 128 + 128.0 * s.bn / s.cg + 6144) / 64;
+        const double tile = (double)num_kb * (mma > load ? mma : load) + 600.0;
+        const double cost = (double)((tiles + units - 1) / units) * tile;
+        if (best_cost < 0 || cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+template <typename OutT, bool NV, int CG>
+static ck_status fp4_launch(const CUtensorMap* maps, const Fp4GemmParams& p, size_t smem, int grid,
+                            bool dep, cudaStream_t stream) {
+    auto kern = fp4_gemm_kernel<OutT, NV, CG>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return CK_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (CG == 2) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (dep) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(fp4g::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = (unsigned)n;
+    if (cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p) != cudaSuccess)
+        return CK_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? CK_OK : CK_ERR_CUDA;
+}
+
+template <typename OutT>
+static ck_status fp4_launch_out(const CUtensorMap* maps, const Fp4GemmParams& p, size_t smem, int grid,
+                                bool nv, int cg, bool dep, cudaStream_t stream) {
+    if (nv)
+        return cg == 2 ? fp4_launch<OutT, true, 2>(maps, p, smem, grid, dep, stream)
+                       : fp4_launch<OutT, true, 1>(maps, p, smem, grid, dep, stream);
+    return cg == 2 ? fp4_launch<OutT, false, 2>(maps, p, smem, grid, dep, stream)
+                   : fp4_launch<OutT, false, 1>(maps, p, smem, grid, dep, stream);
+}
+
+ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream) {
+    using namespace fp4g;
+    const int E = a.offsets ? a.n_experts : 1;
+    const int64_t num_kb = (a.K + BK - 1) / BK;
+    const int64_t k_tiles = fp4_k_tiles(a.K, a.nv);
+    const int sms = num_sms();
+    const Fp4Shape shape = choose_shape(a.M, a.N, num_kb, E, sms);
+    Fp4GemmParams p;
+    p.M = a.M;
+    p.N = a.N;
+    p.num_kb = (int)num_kb;
+    p.k64 = (int)((a.K + 63) / 64);
+    p.BN = shape.bn;
+    p.nblk = shape.bn > 128 ? 2 : 1;
+    p.tiles_n = (int)((a.N + BW * shape.cg - 1) / (BW * shape.cg));
+    // the tile count stays an int: rows split over experts give at most one more tile each
+    if ((double)p.tiles_n * ((double)a.M / p.BN + E + 1) >= 2147483647.0) return CK_ERR_UNSUPPORTED;
+    p.b_bytes = (uint32_t)(shape.bn / shape.cg) * (BK / 2);
+    p.sfa_bytes = (a.nv ? 4 : 2) * kFp4TileBytes;
+    p.sfb_bytes = p.sfa_bytes * p.nblk;
+    p.stage_bytes = (A_BYTES + p.b_bytes + p.sfa_bytes + p.sfb_bytes + 1023) & ~1023u;
+    const size_t fixed = 1024 + EPI_WARPS * EPI_STAGE_BYTES + (size_t)(E + 1) * sizeof(int);
+    p.stages = (int)((SMEM_MAX - fixed) / p.stage_bytes);
+    if (p.stages > STAGES_MAX) p.stages = STAGES_MAX;
+    const size_t smem = fixed + (size_t)p.stages * p.stage_bytes;
+    p.idesc = idesc_fp4(BW * shape.cg, shape.bn, a.nv);
+    p.n_experts = E;
+    p.n_sf_blocks = (int)((a.N + kFp4TileRows - 1) / kFp4TileRows);
+    p.offsets = a.offsets;
+    p.x_ts = a.x_ts;
+    p.w_ts = a.w_ts;
+    p.bias = a.bias;
+    p.bias_dt = a.bias_dt;
+    p.out = a.out;
+    p.ldo = a.ldo;
+    p.dev_status = a.dev_status;
+
+    CUtensorMap maps[4];   // rows, weights, rows' scales, weights' scales
+    const uint64_t half = (uint64_t)(a.K / 2);
+    const uint64_t sf_blocks = (uint64_t)(a.offsets ? a.M / kFp4TileRows + E
+                                                    : (a.M + kFp4TileRows - 1) / kFp4TileRows);
+    const uint64_t tile_words = kFp4TileBytes / 4;
+    const uint32_t sf_tiles = a.nv ? 4 : 2;
+    {
+        const uint64_t dims[2] = {half, (uint64_t)a.M}, strides[1] = {(uint64_t)a.ldq};
+        const uint32_t box[2] = {BK / 2, (uint32_t)(shape.bn / shape.cg)};
+        const ck_status st = encode_tma(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.codes, dims, strides,
+                                        box, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != CK_OK) return st;
+    }
+    {
+        const uint64_t dims[3] = {half, (uint64_t)a.N, (uint64_t)E};
+        const uint64_t strides[2] = {(uint64_t)a.w_ld, (uint64_t)(E > 1 ? a.w_stride : a.w_ld * a.N)};
+        const uint32_t box[3] = {BK / 2, BW, 1};
+        const ck_status st = encode_tma(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.w, dims, strides, box,
+                                        CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != CK_OK) return st;
+    }
+    {
+        const uint64_t dims[3] = {tile_words, (uint64_t)k_tiles, sf_blocks};
+        const uint64_t strides[2] = {kFp4TileBytes, (uint64_t)k_tiles * kFp4TileBytes};
+        const uint32_t box[3] = {(uint32_t)tile_words, sf_tiles, (uint32_t)p.nblk};
+        const ck_status st = encode_tma(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, a.scales, dims, strides,
+                                        box, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (st != CK_OK) return st;
+    }
+    {
+        const uint64_t dims[3] = {tile_words, (uint64_t)k_tiles, (uint64_t)p.n_sf_blocks * (uint64_t)E};
+        const uint64_t strides[2] = {kFp4TileBytes, (uint64_t)k_tiles * kFp4TileBytes};
+        const uint32_t box[3] = {(uint32_t)tile_words, sf_tiles, 1};
+        const ck_status st = encode_tma(&maps[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, a.w_scales, dims,
+                                        strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (st != CK_OK) return st;
+    }
+    // tiles of one matrix are known here; the experts' only on the device
+    int64_t units = sms / shape.cg;
+    if (!a.offsets) {
+        const int64_t tiles = (int64_t)p.tiles_n * ((a.M + p.BN - 1) / p.BN);
+        if (tiles < units) units = tiles;
+    }
+    const int grid = (int)units * shape.cg;
+    switch (a.out_dt) {
+        case CK_F32: return fp4_launch_out<float>(maps, p, smem, grid, a.nv, shape.cg, a.dependent, stream);
+        case CK_F16: return fp4_launch_out<__half>(maps, p, smem, grid, a.nv, shape.cg, a.dependent, stream);
+        case CK_BF16:
+            return fp4_launch_out<__nv_bfloat16>(maps, p, smem, grid, a.nv, shape.cg, a.dependent, stream);
+        default: return CK_ERR_INVALID_ARG;
+    }
+}
+
+}  // namespace ck

@@ -1,0 +1,175 @@
+// ck_fp4_mma.cuh -- tcgen05 operations of the block-scaled fp4 products, for one CTA (CG = 1) or a
+// pair (CG = 2), and the mbarrier operations across a cluster that a pair needs.
+#pragma once
+
+#include <stdint.h>
+
+#include "ck_device.cuh"
+
+namespace ck {
+
+// ------------------------------------------------------------------ mbarriers across a cluster
+
+__device__ __forceinline__ bool mbar_test_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_try_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// mbar_wait for a barrier on which another CTA of the cluster arrives.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                  int* dev_status) {
+    const long long limit = abort ? kRoleWaitLimitCycles : kWaitLimitCycles;
+    if (limit <= 0) {
+        if (mbar_test_cluster(bar, parity)) return true;
+        if (abort) *abort = 1;
+        record_timeout(dev_status);
+        return false;
+    }
+    if (mbar_try_cluster(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_cluster(bar, parity)) return true;
+        if (abort && *abort) return false;
+        if (clock64() - t0 > limit) {
+            if (abort) *abort = 1;
+            record_timeout(dev_status);
+            return false;
+        }
+    }
+}
+
+// Arrive on CTA `rank`'s barrier at the address of `local` in this CTA.
+__device__ __forceinline__ void mbar_arrive_remote(uint64_t* local, uint32_t rank) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+
+// ------------------------------------------------------------------ tensor memory
+
+template <int CG> __device__ __forceinline__ void tmem_alloc_cg(uint32_t* dst_smem, uint32_t ncols) {
+    if (CG == 1) {
+        tmem_alloc(dst_smem, ncols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(dst_smem)),
+                     "r"(ncols)
+                     : "memory");
+    }
+}
+
+template <int CG> __device__ __forceinline__ void tmem_relinquish_cg() {
+    if (CG == 1) tmem_relinquish();
+    else asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+template <int CG> __device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols) {
+    if (CG == 1) {
+        tmem_dealloc(taddr, ncols);
+    } else {
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                     : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ commits
+
+// Arrive on the barrier (of both CTAs of the pair, at the same address) once every tcgen05
+// operation this thread issued so far completes.
+template <int CG> __device__ __forceinline__ void tc_commit_cg(uint64_t* bar) {
+    if (CG == 1) {
+        tc_commit(bar);
+    } else {
+        const uint16_t both = 3;
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+            " [%0], %1;" ::"r"(smem_u32(bar)),
+            "h"(both)
+            : "memory");
+    }
+}
+
+// The same on this CTA's barrier alone.
+template <int CG> __device__ __forceinline__ void tc_commit_local(uint64_t* bar) {
+    if (CG == 1) {
+        tc_commit(bar);
+    } else {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_u32(bar))
+                     : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ scales and MMA
+
+// Shared-memory descriptor of one 512-byte scale tile: 32 rows of 16 bytes without swizzle, 8-row
+// groups 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+    d |= (uint64_t)(128 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    return d;
+}
+
+// One scale tile into four tensor-memory columns: word 4 i + j of the tile goes to lane i, column j
+// of each of the four lane quarters (of both CTAs, each from its own shared memory, for CG = 2).
+template <int CG> __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t sdesc) {
+    if (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Instruction descriptor of tcgen05.mma kind::mxf4nvf4: E2M1 A and B, both K-major, M x N (M over
+// both CTAs of a pair).  Bits: [4,6) B's scale byte, [7,10) A format (1 = E2M1), [10,12) B format,
+// [17,23) N >> 3, [23] scale type (0 = E4M3, 1 = E8M0), [24,29) M >> 4, [29,31) A's scale byte.
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool nv) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((nv ? 0u : 1u) << 23) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T over 64 k, each product times A's and B's block scales in
+// tensor memory: one scale byte per 16 k (NV, four to a word) or 32 k (MX, two to a word).
+template <bool NV, int CG>
+__device__ __forceinline__ void tc_mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                           uint32_t accumulate) {
+#define CK_FP4_MMA(group, vec)                                                                     \
+    asm volatile(                                                                                  \
+        "{\n\t.reg .pred p;\n\t"                                                                   \
+        "setp.ne.b32 p, %6, 0;\n\t"                                                                \
+        "tcgen05.mma.cta_group::" group ".kind::mxf4nvf4.block_scale.scale_vec::" vec              \
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),                                    \
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                  \
+        : "memory")
+    if (NV) {
+        if (CG == 1) CK_FP4_MMA("1", "4X");
+        else CK_FP4_MMA("2", "4X");
+    } else {
+        if (CG == 1) CK_FP4_MMA("1", "2X");
+        else CK_FP4_MMA("2", "2X");
+    }
+#undef CK_FP4_MMA
+}
+
+}  // namespace ck

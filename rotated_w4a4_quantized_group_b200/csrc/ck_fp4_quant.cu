@@ -1,0 +1,449 @@
+// ck_fp4_quant.cu -- activations or weights to microscaled 4-bit floating point, and back.
+//
+//   quantize:   per block of 32 (MX) or 16 (NV) along K: scale from the block's absmax, then
+//               code = e2m1(x / scale); see ck_fp4.cuh for the arithmetic of one block
+//   dequantize: value = cvt(fl(fl(code * scale) * t))
+//
+// Both are one pass over memory, bound by HBM: K * sizeof(x) + K / 2 + K / block bytes a row.
+// A CTA takes 128 rows x 256 channels, so that it owns whole 512-byte scale tiles and writes each
+// of them as one contiguous run from shared memory; a thread takes sixteen channels of a row (an
+// NV block, or half an MX block whose other half is its neighbour lane's), with the loads of
+// several rows in flight.  Column-major input goes through a transposing shared-memory buffer.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "ck_device.cuh"
+#include "ck_fp4.cuh"
+#include "ck_internal.h"
+
+namespace ck {
+
+namespace fp4q {
+constexpr int THREADS = 256;
+constexpr int ROWS = kFp4TileRows;    // rows of a CTA's tile
+constexpr int COLS = 256;             // channels of a CTA's tile
+constexpr int LANES = COLS / 16;      // threads across a row
+constexpr int STEP = THREADS / LANES; // rows a pass of the CTA covers
+constexpr int PASSES = ROWS / STEP;
+constexpr int COL_CHUNK = 64;         // channels a column-major tile transposes at a time
+enum Layout { VEC = 0, ANY = 1, COL = 2 };
+}  // namespace fp4q
+
+struct Fp4QuantParams {
+    const void* x;
+    int64_t M, K, sm, sk;
+    const float* tensor_scale;
+    const int32_t* offsets;   // NULL: one matrix
+    int n_experts;
+    int64_t k_tiles;          // 512-byte scale tiles along K
+    int col_ctas;             // CTAs along K
+    uint8_t* codes;
+    int64_t ldq;
+    bool codes_vec;           // 8-byte code stores
+    uint8_t* scales;
+};
+
+// The rows [row0, row0 + n) of scale block rb: 128 rows of the one matrix, or of the expert whose
+// scale blocks hold rb (n = 0 where no expert's do).
+__device__ __forceinline__ void rows_of_block(const int32_t* offsets, int n_experts, int64_t M,
+                                              int64_t rb, int64_t& row0, int& n) {
+    using namespace fp4q;
+    if (!offsets) {
+        row0 = rb * ROWS;
+        n = (int)((M - row0) < ROWS ? (M - row0) : ROWS);
+        return;
+    }
+    __shared__ int owner;
+    if (threadIdx.x == 0) owner = -1;
+    __syncthreads();
+    for (int e = threadIdx.x; e < n_experts; e += THREADS) {
+        const RowRange r = expert_rows(offsets, e, M);
+        const int64_t b0 = expert_scale_block(r.lo, e);
+        if (rb >= b0 && rb < b0 + (r.hi - r.lo + ROWS - 1) / ROWS) owner = e;
+    }
+    __syncthreads();
+    const int e = owner;
+    row0 = 0;
+    n = 0;
+    if (e >= 0) {
+        const RowRange r = expert_rows(offsets, e, M);
+        row0 = r.lo + (rb - expert_scale_block(r.lo, e)) * ROWS;
+        const int64_t left = r.hi - row0;
+        n = left < 0 ? 0 : (int)(left < ROWS ? left : ROWS);
+    }
+}
+
+// Sixteen consecutive elements at p as loaded words, and as fp32 values.
+template <typename T> struct Raw16 {
+    uint4 u[sizeof(T)];   // 16 elements = sizeof(T) 16-byte words
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) u[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void values(float (&v)[16]) const {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (sizeof(T) == 4) {
+                v[i] = __uint_as_float(w[i]);
+            } else {
+                const uint16_t h = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+                v[i] = Elem<T>::to_f(*reinterpret_cast<const T*>(&h));
+            }
+        }
+    }
+};
+
+// Quantize the sixteen values x of (row r of the tile, channel group g of the tile) into `codes`
+// and the scale byte of its block in the shared scale tiles.  Both lanes of an MX block call it.
+template <bool NV, bool HAS_T>
+__device__ __forceinline__ void quant_group(const float (&x)[16], const Fp4Tensor& t, int r, int g,
+                                            bool valid, uint8_t* sf, uint32_t (&codes)[2]) {
+    uint32_t amax = absmax16(x);
+    if (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const uint32_t byte = fp4_quant16<NV, HAS_T>(x, amax, t, codes);
+    const int c = NV ? g : g >> 1;     // block of the tile's row
+    if (valid && (NV || !(g & 1)))
+        sf[(c >> 2) * kFp4TileBytes + fp4_tile_byte(r, c & 3)] = (uint8_t)byte;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* dst, const uint32_t (&c)[2], bool vec) {
+    if (vec) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dst[i] = (uint8_t)(c[i >> 2] >> (8 * (i & 3)));
+    }
+}
+
+template <typename T, bool NV, bool HAS_T, int LAYOUT>
+__global__ void __launch_bounds__(fp4q::THREADS)
+    fp4_quant_kernel(Fp4QuantParams p) {
+    using namespace fp4q;
+    constexpr int TILES = COLS / 4 / fp4_block(NV);   // scale tiles across the CTA's columns
+    __shared__ __align__(16) uint8_t sf[TILES * kFp4TileBytes];
+    extern __shared__ __align__(16) unsigned char q_smem[];
+    const int tid = threadIdx.x;
+    grid_dependents_launch();
+    for (int i = tid; i < TILES * kFp4TileBytes / 16; i += THREADS)
+        reinterpret_cast<uint4*>(sf)[i] = make_uint4(0, 0, 0, 0);
+
+    const int64_t rb = blockIdx.x / p.col_ctas;
+    const int cc = (int)(blockIdx.x % p.col_ctas);
+    const int64_t k0 = (int64_t)cc * COLS;
+    int64_t row0;
+    int n;
+    rows_of_block(p.offsets, p.n_experts, p.M, rb, row0, n);
+    if (n == 0) return;
+    __syncthreads();   // the cleared scale tiles
+    const Fp4Tensor t = fp4_tensor(HAS_T ? p.tensor_scale : nullptr);
+    const T* x = static_cast<const T*>(p.x);
+
+    if (LAYOUT == COL) {
+        // 64 channels x 128 rows at a time: rows are contiguous in memory, so a warp reads 128 of
+        // them of one channel in a run; a thread then takes sixteen channels of one row, lanes on
+        // neighbouring rows (no bank conflicts: the buffer's row index is fastest)
+        T* buf = reinterpret_cast<T*>(q_smem);                           // [COL_CHUNK][ROWS]
+        uint8_t* cbuf = q_smem + (size_t)COL_CHUNK * ROWS * sizeof(T);   // [ROWS][COLS / 2 + 16]
+        constexpr int CP = COLS / 2 + 16;
+        constexpr int PER = 16 / (int)sizeof(T);                         // elements of 16 bytes
+        const int kmax = (int)((p.K - k0) < COLS ? (p.K - k0) : COLS);
+        for (int c0 = 0; c0 < kmax; c0 += COL_CHUNK) {
+            const int nc = (kmax - c0) < COL_CHUNK ? (kmax - c0) : COL_CHUNK;
+            if (n == ROWS && reinterpret_cast<uintptr_t>(x + row0) % 16 == 0 &&
+                (p.sk * (int64_t)sizeof(T)) % 16 == 0) {
+                constexpr int N16 = ROWS / PER;
+#pragma unroll 8
+                for (int i = tid; i < COL_CHUNK * N16; i += THREADS) {
+                    const int c = i / N16, m = (i % N16) * PER;
+                    if (c < nc)
+                        *reinterpret_cast<uint4*>(buf + c * ROWS + m) = __ldg(reinterpret_cast<const uint4*>(
+                            x + row0 + m + (k0 + c0 + c) * p.sk));
+                }
+            } else {
+                for (int i = tid; i < nc * ROWS; i += THREADS) {
+                    const int c = i / ROWS, m = i % ROWS;
+                    if (m < n) buf[c * ROWS + m] = x[row0 + m + (k0 + c0 + c) * p.sk];
+                }
+            }
+            __syncthreads();
+            if (NV) {
+                for (int i = tid; i < nc / 16 * ROWS; i += THREADS) {
+                    const int g = i / ROWS, r = i % ROWS;
+                    if (r < n) {
+                        float v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = Elem<T>::to_f(buf[(g * 16 + j) * ROWS + r]);
+                        uint32_t c[2];
+                        const uint32_t byte = fp4_quant16<NV, HAS_T>(v, absmax16(v), t, c);
+                        const int b = c0 / 16 + g;
+                        sf[(b >> 2) * kFp4TileBytes + fp4_tile_byte(r, b & 3)] = (uint8_t)byte;
+                        store_codes(cbuf + r * CP + (c0 + g * 16) / 2, c, true);
+                    }
+                }
+            } else {
+                for (int i = tid; i < nc / 32 * ROWS; i += THREADS) {
+                    const int g = i / ROWS, r = i % ROWS;
+                    if (r < n) {
+                        float v[2][16];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j >> 4][j & 15] = Elem<T>::to_f(buf[(g * 32 + j) * ROWS + r]);
+                        const uint32_t amax = max(absmax16(v[0]), absmax16(v[1]));
+                        uint32_t c[2], byte = 0;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            byte = fp4_quant16<NV, HAS_T>(v[h], amax, t, c);
+                            store_codes(cbuf + r * CP + (c0 + g * 32 + 16 * h) / 2, c, true);
+                        }
+                        const int b = c0 / 32 + g;
+                        sf[(b >> 2) * kFp4TileBytes + fp4_tile_byte(r, b & 3)] = (uint8_t)byte;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        // the rows' codes, eight bytes a thread
+        const int pieces = kmax / 16;
+        for (int i = tid; i < ROWS * LANES; i += THREADS) {
+            const int r = i / LANES, c = i % LANES;
+            if (r < n && c < pieces) {
+                const uint2 u = *reinterpret_cast<const uint2*>(cbuf + r * CP + c * 8);
+                const uint32_t w[2] = {u.x, u.y};
+                store_codes(p.codes + (row0 + r) * p.ldq + k0 / 2 + c * 8, w, p.codes_vec);
+            }
+        }
+    } else {
+        const int g = tid % LANES, r0 = tid / LANES;
+        const int64_t k = k0 + g * 16;
+        const bool k_ok = k < p.K;
+        // K is a multiple of the block: a group of sixteen is whole, and so is an MX pair
+        constexpr int AHEAD = sizeof(T) == 4 ? 2 : 4;   // rows whose loads are in flight
+        if (LAYOUT == VEC) {
+#pragma unroll 1
+            for (int it = 0; it < PASSES; it += AHEAD) {
+                if (it * STEP >= n) break;
+                Raw16<T> raw[AHEAD];
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a) {
+                    const int r = (it + a) * STEP + r0;
+                    if (k_ok && r < n) raw[a].load(x + (row0 + r) * p.sm + k);
+                    else raw[a].zero();
+                }
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a) {
+                    const int r = (it + a) * STEP + r0;
+                    float v[16];
+                    raw[a].values(v);
+                    uint32_t c[2];
+                    quant_group<NV, HAS_T>(v, t, r, g, k_ok && r < n, sf, c);
+                    if (k_ok && r < n)
+                        store_codes(p.codes + (row0 + r) * p.ldq + k / 2, c, p.codes_vec);
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int it = 0; it < PASSES; ++it) {
+                if (it * STEP >= n) break;
+                const int r = it * STEP + r0;
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] = k_ok && r < n ? Elem<T>::to_f(x[(row0 + r) * p.sm + (k + j) * p.sk]) : 0.0f;
+                uint32_t c[2];
+                quant_group<NV, HAS_T>(v, t, r, g, k_ok && r < n, sf, c);
+                if (k_ok && r < n)
+                    store_codes(p.codes + (row0 + r) * p.ldq + k / 2, c, p.codes_vec);
+            }
+        }
+    }
+    __syncthreads();
+    // the CTA's scale tiles: one contiguous run, zero past the last row and block
+    const int64_t t0 = (int64_t)cc * TILES;
+    const int nt = (int)((p.k_tiles - t0) < TILES ? (p.k_tiles - t0) : TILES);
+    uint4* dst = reinterpret_cast<uint4*>(p.scales + (rb * p.k_tiles + t0) * kFp4TileBytes);
+    for (int i = tid; i < nt * kFp4TileBytes / 16; i += THREADS)
+        dst[i] = reinterpret_cast<const uint4*>(sf)[i];
+}
+
+struct Fp4DequantParams {
+    const uint8_t* codes;
+    int64_t ldq;
+    const uint8_t* scales;
+    int64_t M, K;
+    const float* tensor_scale;
+    const int32_t* offsets;
+    int n_experts;
+    int64_t k_tiles;
+    int col_ctas;
+    bool codes_vec, out_vec;
+    void* out;
+    int64_t ldo;
+};
+
+template <typename T, bool NV>
+__global__ void __launch_bounds__(fp4q::THREADS)
+    fp4_dequant_kernel(Fp4DequantParams p) {
+    using namespace fp4q;
+    constexpr int TILES = COLS / 4 / fp4_block(NV);
+    __shared__ __align__(16) uint8_t sf[TILES * kFp4TileBytes];
+    const int tid = threadIdx.x;
+    const int64_t rb = blockIdx.x / p.col_ctas;
+    const int cc = (int)(blockIdx.x % p.col_ctas);
+    int64_t row0;
+    int n;
+    rows_of_block(p.offsets, p.n_experts, p.M, rb, row0, n);
+    if (n == 0) return;
+    const int64_t t0 = (int64_t)cc * TILES;
+    const int nt = (int)((p.k_tiles - t0) < TILES ? (p.k_tiles - t0) : TILES);
+    const uint4* src = reinterpret_cast<const uint4*>(p.scales + (rb * p.k_tiles + t0) * kFp4TileBytes);
+    for (int i = tid; i < nt * kFp4TileBytes / 16; i += THREADS)
+        reinterpret_cast<uint4*>(sf)[i] = __ldg(src + i);
+    __syncthreads();
+    const float t = p.tensor_scale ? __ldg(p.tensor_scale) : 1.0f;
+    const int g = tid % LANES, r0 = tid / LANES;
+    const int64_t k = (int64_t)cc * COLS + g * 16;
+    if (k >= p.K) return;
+    const int c = NV ? g : g >> 1;
+    T* out = static_cast<T*>(p.out);
+#pragma unroll 4
+    for (int it = 0; it < PASSES; ++it) {
+        const int r = it * STEP + r0;
+        if (r >= n) break;
+        const uint8_t* src8 = p.codes + (row0 + r) * p.ldq + k / 2;
+        uint32_t w[2];
+        if (p.codes_vec) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(src8));
+            w[0] = u.x;
+            w[1] = u.y;
+        } else {
+            w[0] = w[1] = 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)__ldg(src8 + i) << (8 * (i & 3));
+        }
+        const uint32_t byte = sf[(c >> 2) * kFp4TileBytes + fp4_tile_byte(r, c & 3)];
+        const float s = NV ? e4m3_value(byte) : e8m0_value(byte);
+        T* dst = out + (row0 + r) * p.ldo + k;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            fp4_unpack8(w[h], v);
+            __align__(16) T o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)   // code * scale is exact: at most six significant bits
+                o[i] = Elem<T>::from_f(__fmul_rn(__fmul_rn(v[i], s), t));
+            if (p.out_vec) {
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+                    reinterpret_cast<uint4*>(dst + 8 * h)[i] = reinterpret_cast<const uint4*>(o)[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[8 * h + i] = o[i];
+            }
+        }
+    }
+}
+
+static int64_t row_blocks(int64_t M, const int32_t* offsets, int n_experts) {
+    return offsets ? M / kFp4TileRows + n_experts : (M + kFp4TileRows - 1) / kFp4TileRows;
+}
+
+template <typename T, bool NV, bool HAS_T>
+static ck_status quant_launch(const Fp4QuantParams& p, int64_t grid, cudaStream_t stream) {
+    using namespace fp4q;
+    const int64_t eb = sizeof(T);
+    if (p.sk == 1 && aligned(p.x, 16) && p.sm * eb % 16 == 0) {
+        fp4_quant_kernel<T, NV, HAS_T, VEC><<<(unsigned)grid, THREADS, 0, stream>>>(p);
+    } else if (p.sm == 1 && p.M >= 32) {
+        // the channel runs of at least 32 rows are worth the transposing buffer
+        constexpr int smem = COL_CHUNK * ROWS * (int)sizeof(T) + ROWS * (COLS / 2 + 16);
+        auto kern = fp4_quant_kernel<T, NV, HAS_T, COL>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return CK_ERR_CUDA;
+        kern<<<(unsigned)grid, THREADS, smem, stream>>>(p);
+    } else {
+        fp4_quant_kernel<T, NV, HAS_T, ANY><<<(unsigned)grid, THREADS, 0, stream>>>(p);
+    }
+    return cudaGetLastError() == cudaSuccess ? CK_OK : CK_ERR_CUDA;
+}
+
+template <typename T>
+static ck_status quant_typed(const Fp4QuantParams& p, bool nv, int64_t grid, cudaStream_t stream) {
+    if (!nv) return quant_launch<T, false, false>(p, grid, stream);
+    if (p.tensor_scale) return quant_launch<T, true, true>(p, grid, stream);
+    return quant_launch<T, true, false>(p, grid, stream);
+}
+
+ck_status launch_quant_fp4(const void* x, ck_dtype dt, int64_t M, int64_t K, int64_t sm, int64_t sk,
+                           bool nv, const float* tensor_scale, const int32_t* offsets, int n_experts,
+                           uint8_t* codes, int64_t ldq, uint8_t* scales, cudaStream_t stream) {
+    Fp4QuantParams p;
+    p.x = x;
+    p.M = M;
+    p.K = K;
+    p.sm = sm;
+    p.sk = sk;
+    p.tensor_scale = tensor_scale;
+    p.offsets = offsets;
+    p.n_experts = n_experts;
+    p.k_tiles = fp4_k_tiles(K, nv);
+    p.codes = codes;
+    p.ldq = ldq;
+    p.codes_vec = aligned(codes, 8) && ldq % 8 == 0;
+    p.scales = scales;
+    const int64_t cols = (K + fp4q::COLS - 1) / fp4q::COLS;
+    const int64_t grid = cols * row_blocks(M, offsets, n_experts);
+    if (grid >= (1LL << 31)) return CK_ERR_UNSUPPORTED;
+    p.col_ctas = (int)cols;
+    switch (dt) {
+        case CK_F32: return quant_typed<float>(p, nv, grid, stream);
+        case CK_F16: return quant_typed<__half>(p, nv, grid, stream);
+        case CK_BF16: return quant_typed<__nv_bfloat16>(p, nv, grid, stream);
+        default: return CK_ERR_INVALID_ARG;
+    }
+}
+
+template <typename T>
+static void dequant_typed(const Fp4DequantParams& p, bool nv, int64_t grid, cudaStream_t stream) {
+    if (nv) fp4_dequant_kernel<T, true><<<(unsigned)grid, fp4q::THREADS, 0, stream>>>(p);
+    else fp4_dequant_kernel<T, false><<<(unsigned)grid, fp4q::THREADS, 0, stream>>>(p);
+}
+
+ck_status launch_dequant_fp4(const uint8_t* codes, int64_t ldq, const uint8_t* scales, int64_t M,
+                             int64_t K, bool nv, const float* tensor_scale, const int32_t* offsets,
+                             int n_experts, void* out, ck_dtype out_dt, int64_t ldo,
+                             cudaStream_t stream) {
+    const int64_t eb = out_dt == CK_F32 ? 4 : 2;
+    Fp4DequantParams p;
+    p.codes = codes;
+    p.ldq = ldq;
+    p.scales = scales;
+    p.M = M;
+    p.K = K;
+    p.tensor_scale = tensor_scale;
+    p.offsets = offsets;
+    p.n_experts = n_experts;
+    p.k_tiles = fp4_k_tiles(K, nv);
+    p.codes_vec = aligned(codes, 8) && ldq % 8 == 0;
+    p.out_vec = aligned(out, 16) && ldo * eb % 16 == 0;
+    p.out = out;
+    p.ldo = ldo;
+    const int64_t cols = (K + fp4q::COLS - 1) / fp4q::COLS;
+    const int64_t grid = cols * row_blocks(M, offsets, n_experts);
+    if (grid >= (1LL << 31)) return CK_ERR_UNSUPPORTED;
+    p.col_ctas = (int)cols;
+    switch (out_dt) {
+        case CK_F32: dequant_typed<float>(p, nv, grid, stream); break;
+        case CK_F16: dequant_typed<__half>(p, nv, grid, stream); break;
+        case CK_BF16: dequant_typed<__nv_bfloat16>(p, nv, grid, stream); break;
+        default: return CK_ERR_INVALID_ARG;
+    }
+    return cudaGetLastError() == cudaSuccess ? CK_OK : CK_ERR_CUDA;
+}
+
+}  // namespace ck

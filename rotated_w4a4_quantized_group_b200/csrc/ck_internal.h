@@ -122,6 +122,40 @@ ck_status launch_rotate_quant_packed(const void* x, ck_dtype dt, int64_t M, int6
                                      uint8_t* packed, int64_t ldp, float* scales,
                                      cudaStream_t stream);
 
+// Microscaled fp4 (ck_fp4_quant.cu), arguments already validated; nv: CK_NVFP4, else CK_MXFP4.
+// offsets NULL: one matrix; otherwise n_experts + 1 device offsets of the experts' rows.
+ck_status launch_quant_fp4(const void* x, ck_dtype dt, int64_t M, int64_t K, int64_t sm, int64_t sk,
+                           bool nv, const float* tensor_scale, const int32_t* offsets, int n_experts,
+                           uint8_t* codes, int64_t ldq, uint8_t* scales, cudaStream_t stream);
+ck_status launch_dequant_fp4(const uint8_t* codes, int64_t ldq, const uint8_t* scales, int64_t M,
+                             int64_t K, bool nv, const float* tensor_scale, const int32_t* offsets,
+                             int n_experts, void* out, ck_dtype out_dt, int64_t ldo,
+                             cudaStream_t stream);
+
+// The product of fp4 rows and fp4 weights, arguments already validated.
+struct Fp4Product {
+    const uint8_t* codes;      // (M, K / 2), 16-byte-aligned rows
+    int64_t ldq;
+    const uint8_t* scales;     // the rows' scale tiles
+    int64_t M, K;
+    bool nv;
+    const float* x_ts;         // NULL: one
+    const int32_t* offsets;    // NULL: one matrix
+    int n_experts;
+    const uint8_t* w;          // (n_experts, N, K / 2), 16-byte-aligned rows and matrices
+    int64_t N, w_ld, w_stride;
+    const uint8_t* w_scales;   // each matrix's scale tiles, one after the other
+    const float* w_ts;         // (n_experts,), NULL: one
+    const void* bias;          // (n_experts, N), NULL: none
+    ck_dtype bias_dt;
+    void* out;
+    ck_dtype out_dt;
+    int64_t ldo;
+    bool dependent;            // the kernel right before on the stream wrote codes and scales
+    int* dev_status;
+};
+ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream);   // ck_fp4_gemm.cu
+
 // Copy a (rows, cols) byte matrix between pitches (used to re-pitch misaligned inputs).
 ck_status launch_copy_rows(const int8_t* src, int64_t ld_src, int8_t* dst, int64_t ld_dst,
                            int64_t rows, int64_t cols, cudaStream_t stream);

@@ -15,8 +15,7 @@
 //            scale tiles; the weights' part of the first stages before the wait for the kernel
 //            before this one (the quantizer)
 //   warp 1   copies the scale tiles from shared to tensor memory (tcgen05.cp, in order with the
-//            MMAs that read them) and issues the MMAs: the CTA of rank 0 for both CTAs.  The other
-//            CTA's warp 1 forwards "stage full" to rank 0 instead.
+//            MMAs that read them) and issues the MMAs: the CTA of rank 0 for both CTAs
 //   warps 4-11  the epilogue: two warps per lane quarter on alternate 16-row chunks, from one of
 //            two accumulators while the MMAs fill the other; outputs transposed through a staging
 //            buffer into 16-byte stores
@@ -135,11 +134,12 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     unsigned char* epi_stage = ring + (size_t)S * p.stage_bytes;
     int* cum = reinterpret_cast<int*>(epi_stage + EPI_WARPS * EPI_STAGE_BYTES);   // [n_experts + 1]
 
-    __shared__ __align__(8) uint64_t full[STAGES_MAX], peer_full[STAGES_MAX], empty[STAGES_MAX];
+    __shared__ __align__(8) uint64_t full[STAGES_MAX], empty[STAGES_MAX];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain_bar;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     __shared__ uint32_t commits[2];          // rank 0's count of stage and of accumulator commits
+    __shared__ uint32_t loaded;              // stages whose loads this CTA issued
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
@@ -148,7 +148,6 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     if (tid == 0) {
         for (int s = 0; s < STAGES_MAX; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&peer_full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
         }
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
-        commits[0] = commits[1] = 0;
+        commits[0] = commits[1] = loaded = 0;
         fence_mbar_init();
         tma_prefetch_desc(&xmap);
         tma_prefetch_desc(&wmap);
@@ -200,28 +199,32 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     const uint32_t tmem_base = tmem_base_sh;
     const int tiles = cum[p.n_experts];
     const uint32_t num_kb = (uint32_t)p.num_kb;
+    const uint32_t load_bytes = A_BYTES + p.b_bytes + p.sfa_bytes + p.sfb_bytes;   // a CTA's, a stage
+    const uint32_t full0 = CG == 2 ? cluster_address(&full[0], 0) : smem_u32(&full[0]);
     const uint32_t my_tiles = tiles > unit ? (uint32_t)((tiles - unit + units - 1) / units) : 0u;
     const uint32_t my_stages = my_tiles * num_kb;
 
     if (warp == WARP_TMA) {
         // ---------------------------------------------------------------- loads
+        // both CTAs' copies of a stage complete on rank 0's barrier, which rank 0 arms for both
         if (lane == 0) {
             uint32_t issued = 0;
-            bool ok = true;
             auto load_w = [&](const Fp4Tile& t, uint32_t kb, uint32_t s) {
                 unsigned char* st = ring + (size_t)s * p.stage_bytes;
-                mbar_arrive_expect_tx(&full[s], A_BYTES + p.b_bytes + p.sfa_bytes + p.sfb_bytes);
-                tma_load_3d(st, &wmap, &full[s], (int32_t)(kb * (BK / 2)),
-                            (int32_t)t.n0 + (int32_t)rank * BW, t.e);
-                tma_load_3d(st + A_BYTES + p.b_bytes, &wsmap, &full[s], 0, (int32_t)(kb * SF_TILES),
-                            t.e * p.n_sf_blocks + (int)(t.n0 / BW) + (int)rank);
+                const uint32_t bar = full0 + s * 8;
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * load_bytes);
+                tma_load_3d_cg<CG>(st, &wmap, bar, (int32_t)(kb * (BK / 2)),
+                                   (int32_t)t.n0 + (int32_t)rank * BW, t.e);
+                tma_load_3d_cg<CG>(st + A_BYTES + p.b_bytes, &wsmap, bar, 0, (int32_t)(kb * SF_TILES),
+                                   t.e * p.n_sf_blocks + (int)(t.n0 / BW) + (int)rank);
             };
             auto load_x = [&](const Fp4Tile& t, uint32_t kb, uint32_t s) {
                 unsigned char* st = ring + (size_t)s * p.stage_bytes;
-                tma_load_2d(st + A_BYTES, &xmap, &full[s], (int32_t)(kb * (BK / 2)),
-                            (int32_t)t.m0 + (int32_t)rank * (p.BN / CG));
-                tma_load_3d(st + A_BYTES + p.b_bytes + p.sfa_bytes, &xsmap, &full[s], 0,
-                            (int32_t)(kb * SF_TILES), t.sf_block);
+                const uint32_t bar = full0 + s * 8;
+                tma_load_2d_cg<CG>(st + A_BYTES, &xmap, bar, (int32_t)(kb * (BK / 2)),
+                                   (int32_t)t.m0 + (int32_t)rank * (p.BN / CG));
+                tma_load_3d_cg<CG>(st + A_BYTES + p.b_bytes + p.sfa_bytes, &xsmap, bar, 0,
+                                   (int32_t)(kb * SF_TILES), t.sf_block);
             };
             // the weights of the first stages, then the rows once the kernel before has written them
             const uint32_t head = my_stages < S ? my_stages : S;
@@ -241,10 +244,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
             for (uint32_t i = 0; i < my_stages; ++i) {
                 if (kb == 0) t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
                 if (i >= head) {
-                    if (!mbar_wait_cluster(&empty[s], phase ^ 1u, &abort_flag, p.dev_status)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!mbar_wait(&empty[s], phase ^ 1u, &abort_flag, p.dev_status)) break;
                     load_w(t, kb, s);
                 }
                 load_x(t, kb, s);
@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
                     phase ^= 1u;
                 }
             }
-            if (!ok)   // copies in flight land before the CTA leaves
-                for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
-                    mbar_wait(&full[j % S], (j / S) & 1u, nullptr, nullptr);
+            // the weights' part of a head stage is in flight even where its rows' part is not: the
+            // loop above issues every head stage's, as nothing makes it stop before
+            loaded = issued;
         }
         __syncwarp();
     } else if (warp == WARP_MMA && rank == 0) {
@@ -280,9 +280,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
             tc_fence_after();
             const uint32_t d = tmem_base + acc * BN_MAX;
             for (uint32_t kb = 0; kb < num_kb; ++kb) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, &abort_flag, p.dev_status)) ||
-                    (CG == 2 && !__all_sync(0xffffffffu, mbar_wait_cluster(&peer_full[s], phase, &abort_flag,
-                                                                           p.dev_status)))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, &abort_flag, p.dev_status))) {
                     ok = false;
                     break;
                 }
@@ -331,19 +329,6 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
             commits[1] = n_acc;
         }
         __syncwarp();
-    } else if (CG == 2 && warp == WARP_MMA) {
-        // ---------------------------------------------------------------- forward "full" to rank 0
-        grid_dependency_wait();
-        uint32_t s = 0, phase = 0;
-        for (uint32_t i = 0; i < my_stages; ++i) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, &abort_flag, p.dev_status))) break;
-            if (lane == 0) mbar_arrive_remote(&peer_full[s], 0);
-            if (++s == S) {
-                s = 0;
-                phase ^= 1u;
-            }
-        }
-        __syncwarp();
     } else if (warp >= EPI_WARP0) {
         // ---------------------------------------------------------------- epilogue
         const int q = warp & 3;                        // TMEM lanes 32q .. 32q + 31
@@ -357,8 +342,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
             const bool n_ok = n < p.N;
             const float alpha = __fmul_rn(xts, p.w_ts ? __ldg(p.w_ts + t.e) : 1.0f);
             const float bs = p.bias && n_ok ? load_any(p.bias, p.bias_dt, (int64_t)t.e * p.N + n) : 0.0f;
-            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[acc], (lt >> 1) & 1u, &abort_flag,
-                                                           p.dev_status)))
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], (lt >> 1) & 1u, &abort_flag, p.dev_status)))
                 break;
             tc_fence_after();
             const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN_MAX;
@@ -403,20 +387,30 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) {
-        // rank 0's MMAs have completed (its drain) and its counts are readable: wait for the
-        // arrivals of its commits at this CTA's barriers, then for the peer to have done the same
-        cluster_sync_all();
-        if (tid == 0) {
+    if (CG == 2) cluster_sync_all();   // rank 0's MMAs have completed, and the counts are readable
+    if (tid == 0) {
+        if (rank == 0) {
+            // every copy has landed: where only one CTA issued a stage's (after a timeout), the
+            // barrier is told so
+            const uint32_t mine = loaded, other = CG == 2 ? dsmem_load_u32(&loaded, 1) : mine;
+            const uint32_t n = mine > other ? mine : other;
+            for (uint32_t j = n > S ? n - S : 0; j < n; ++j) {
+                if (j >= mine) mbar_arrive_expect_tx(&full[j % S], load_bytes);
+                else if (j >= other) mbar_complete_tx(&full[j % S], load_bytes);
+                mbar_wait(&full[j % S], (j / S) & 1u, nullptr, p.dev_status);
+            }
+        }
+        if (CG == 2) {
+            // the arrivals of rank 0's commits at this CTA's barriers have come
             const uint32_t n = dsmem_load_u32(&commits[0], 0), a = dsmem_load_u32(&commits[1], 0);
             for (uint32_t j = n > S ? n - S : 0; j < n; ++j)
-                mbar_wait_cluster(&empty[j % S], (j / S) & 1u, nullptr, nullptr);
+                mbar_wait(&empty[j % S], (j / S) & 1u, nullptr, p.dev_status);
             for (uint32_t j = a > 2 ? a - 2 : 0; j < a; ++j)
-                mbar_wait_cluster(&acc_full[j & 1u], (j >> 1) & 1u, nullptr, nullptr);
+                mbar_wait(&acc_full[j & 1u], (j >> 1) & 1u, nullptr, p.dev_status);
         }
-        __syncthreads();
-        cluster_sync_all();
     }
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();
     if (warp == WARP_MMA) {
         tc_fence_after();
         tmem_dealloc_cg<CG>(tmem_base, TMEM_COLS);

@@ -16,9 +16,8 @@
 //            before this one (the quantizer)
 //   warp 1   copies the scale tiles from shared to tensor memory (tcgen05.cp, in order with the
 //            MMAs that read them) and issues the MMAs: the CTA of rank 0 for both CTAs
-//   warps 4-11  the epilogue: two warps per lane quarter on alternate 16-row chunks, from one of
-//            two accumulators while the MMAs fill the other; outputs transposed through a staging
-//            buffer into 16-byte stores
+//   warps 4-11  the epilogue: two warps per lane quarter on alternate 32-row chunks, from one of
+//            two accumulators while the MMAs fill the other
 // Every wait is bounded; a CTA leaves only after its own copies have landed, the MMAs that read
 // its memory have completed and the arrivals that were sent to it have come.
 #include <cuda.h>
@@ -45,10 +44,22 @@ constexpr uint32_t A_BYTES = BW * BK / 2;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t SF_COL = 2 * BN_MAX;   // two accumulators, then two sets of scale columns
 constexpr uint32_t SF_SET = 48;
-constexpr int EPI_STAGE_BYTES = 16 * 32 * 4;
+constexpr int EPI_STAGE_BYTES = 32 * 32 * 2;
 constexpr size_t SMEM_MAX = 227 * 1024 - 1024;   // less the static shared memory
 static_assert(SF_COL + 2 * SF_SET <= TMEM_COLS, "accumulators and scales fit");
 }  // namespace fp4g
+
+template <typename OutT> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return 0u;   // fp32 outputs are not packed
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 struct Fp4GemmParams {
     int64_t M, N;
@@ -119,6 +130,71 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4GemmParams& p, const int* c
     return r;
 }
 
+// 32 rows (tensor-memory columns from taddr on) x 32 channels (lanes) of 16-bit outputs: loaded as
+// 8 x 8 fragments, whose pairs of neighbouring rows pack into one register, and stored transposed
+// (stmatrix) into the staging buffer, whose rows then leave in 16-byte pieces.  64-byte staging rows;
+// piece c of row m sits at c ^ (m / 2 % 4), so that neither side meets a bank twice.  b: the biases
+// of channels lane / 4 + 8 i.
+template <typename OutT>
+__device__ __forceinline__ void epilogue_vec(uint32_t taddr, float alpha, const float (&b)[4], bool bias,
+                                             unsigned char* stage, int lane, OutT* out, int64_t ldo,
+                                             int rows) {
+    uint32_t r[2][16];
+    tc_ld_16x256b_x4(taddr, r[0]);
+    tc_ld_16x256b_x4(taddr + (16u << 16), r[1]);
+    tc_wait_ld();
+    const uint32_t base = smem_u32(stage);
+    const int mat = lane >> 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t u[8];   // [4 row groups of 8][channels 16 h.., 16 h + 8..]
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float x = __fmul_rn(__uint_as_float(r[h][2 * i]), alpha);
+            float y = __fmul_rn(__uint_as_float(r[h][2 * i + 1]), alpha);
+            if (bias) {
+                x = __fadd_rn(x, b[2 * h + (i & 1)]);
+                y = __fadd_rn(y, b[2 * h + (i & 1)]);
+            }
+            u[i] = pack2<OutT>(x, y);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const int m = 8 * (i + (mat >> 1)) + (lane & 7);
+            const int c = (2 * h + (mat & 1)) ^ ((m >> 1) & 3);
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                             base + (uint32_t)(m * 64 + c * 16)),
+                         "r"(u[2 * i]), "r"(u[2 * i + 1]), "r"(u[2 * i + 2]), "r"(u[2 * i + 3])
+                         : "memory");
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = 8 * i + (lane >> 2), c = lane & 3;
+        if (m < rows)
+            *reinterpret_cast<uint4*>(out + m * ldo + c * 8) =
+                *reinterpret_cast<const uint4*>(stage + m * 64 + ((c ^ ((m >> 1) & 3)) << 4));
+    }
+    __syncwarp();
+}
+
+// The same for fp32 outputs, whose 32 channels of a row are one 128-byte store of the warp as they
+// are, and for 16-bit rows that 16-byte stores do not fit: a lane is a channel.
+template <typename OutT>
+__device__ __forceinline__ void epilogue_any(uint32_t taddr, float alpha, float b, bool bias, bool n_ok,
+                                             OutT* out, int64_t ldo, int rows) {
+    uint32_t r[32];
+    tc_ld_32x32b_x32(taddr, r);
+    tc_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        float o = __fmul_rn(__uint_as_float(r[j]), alpha);
+        if (bias) o = __fadd_rn(o, b);
+        if (n_ok && j < rows) OutStore<OutT>::one(out + j * ldo, o);
+    }
+}
+
 template <typename OutT, bool NV, int CG>
 __global__ void __launch_bounds__(fp4g::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap xmap,
@@ -135,7 +211,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     int* cum = reinterpret_cast<int*>(epi_stage + EPI_WARPS * EPI_STAGE_BYTES);   // [n_experts + 1]
 
     __shared__ __align__(8) uint64_t full[STAGES_MAX], empty[STAGES_MAX];
-    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain_bar;
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], acc_read[2], drain_bar;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     __shared__ uint32_t commits[2];          // rank 0's count of stage and of accumulator commits
@@ -152,7 +228,8 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], EPI_WARPS * CG);
+            mbar_init(&acc_empty[s], EPI_WARPS + CG - 1);   // and the other CTA's word
+            mbar_init(&acc_read[s], EPI_WARPS);
         }
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
@@ -329,59 +406,52 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
             commits[1] = n_acc;
         }
         __syncwarp();
+    } else if (CG == 2 && warp == WARP_MMA) {
+        // ---------------------------------------------------------------- the other CTA's epilogue
+        // tells rank 0 that this CTA has read an accumulator: an arrival that reaches the other SM
+        // waits for its thread's earlier stores, so the epilogue's warps leave it to this one
+        grid_dependency_wait();
+        for (uint32_t lt = 0; lt < my_tiles; ++lt) {
+            const uint32_t acc = lt & 1u;
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_read[acc], (lt >> 1) & 1u, &abort_flag, p.dev_status)))
+                break;
+            if (lane == 0) mbar_arrive_remote(&acc_empty[acc], 0);
+        }
+        __syncwarp();
     } else if (warp >= EPI_WARP0) {
         // ---------------------------------------------------------------- epilogue
         const int q = warp & 3;                        // TMEM lanes 32q .. 32q + 31
-        const int eh = (warp - EPI_WARP0) >> 2;        // 16-row chunks eh, eh + 2, ...
+        const int eh = (warp - EPI_WARP0) >> 2;        // 32-row chunks eh, eh + 2, ...
+        unsigned char* stage = epi_stage + (size_t)(warp - EPI_WARP0) * EPI_STAGE_BYTES;
         grid_dependency_wait();
         const float xts = p.x_ts ? __ldg(p.x_ts) : 1.0f;
         for (uint32_t lt = 0; lt < my_tiles; ++lt) {
             const Fp4Tile t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
             const uint32_t acc = lt & 1u;
-            const int64_t n = t.n0 + (int64_t)rank * BW + q * 32 + lane;
-            const bool n_ok = n < p.N;
+            const int64_t n = t.n0 + (int64_t)rank * BW + q * 32;   // the warp's first channel
             const float alpha = __fmul_rn(xts, p.w_ts ? __ldg(p.w_ts + t.e) : 1.0f);
-            const float bs = p.bias && n_ok ? load_any(p.bias, p.bias_dt, (int64_t)t.e * p.N + n) : 0.0f;
+            OutT* ocol = static_cast<OutT*>(p.out) + t.m0 * p.ldo + n;
+            const bool vec = sizeof(OutT) == 2 && n + 32 <= p.N && p.ldo % 8 == 0 &&
+                             reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+            float bs[4];   // vec: channels lane / 4 + 8 i, otherwise channel lane in bs[0]
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t ch = n + (vec ? lane / 4 + 8 * i : lane);
+                bs[i] = p.bias && ch < p.N ? load_any(p.bias, p.bias_dt, (int64_t)t.e * p.N + ch) : 0.0f;
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], (lt >> 1) & 1u, &abort_flag, p.dev_status)))
                 break;
             tc_fence_after();
             const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN_MAX;
-            OutT* obase = static_cast<OutT*>(p.out) + (n - lane);   // the warp's first channel
-            constexpr int PER16 = 16 / (int)sizeof(OutT);
-            const bool vec = n - lane + 32 <= p.N && reinterpret_cast<uintptr_t>(obase) % 16 == 0 &&
-                             p.ldo % PER16 == 0;
-            OutT* stage = reinterpret_cast<OutT*>(epi_stage + (size_t)(warp - EPI_WARP0) * EPI_STAGE_BYTES);
-            for (int c0 = 16 * eh; c0 < t.rows; c0 += 32) {
-                uint32_t r[16];
-                tc_ld_32x32b_x16(tacc + (uint32_t)c0, r);
-                tc_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float o = __fmul_rn(__uint_as_float(r[j]), alpha);
-                    if (p.bias) o = __fadd_rn(o, bs);
-                    if (vec) OutStore<OutT>::one(stage + j * 32 + lane, o);
-                    else if (c0 + j < t.rows && n_ok)
-                        OutStore<OutT>::one(obase + lane + (t.m0 + c0 + j) * p.ldo, o);
-                }
-                if (vec) {
-                    __syncwarp();
-                    constexpr int PIECES = 32 / PER16;
-#pragma unroll
-                    for (int i = lane; i < 16 * PIECES; i += 32) {
-                        const int row = i / PIECES, pc = i % PIECES;
-                        if (c0 + row < t.rows)
-                            *reinterpret_cast<uint4*>(obase + (t.m0 + c0 + row) * p.ldo + pc * PER16) =
-                                *reinterpret_cast<const uint4*>(stage + row * 32 + pc * PER16);
-                    }
-                    __syncwarp();
-                }
+            for (int c0 = 32 * eh; c0 < t.rows; c0 += 64) {
+                if (vec) epilogue_vec<OutT>(tacc + (uint32_t)c0, alpha, bs, p.bias != nullptr, stage, lane,
+                                            ocol + c0 * p.ldo, p.ldo, t.rows - c0);
+                else epilogue_any<OutT>(tacc + (uint32_t)c0, alpha, bs[0], p.bias != nullptr,
+                                        n + lane < p.N, ocol + lane + c0 * p.ldo, p.ldo, t.rows - c0);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                if (CG == 2 && rank != 0) mbar_arrive_remote(&acc_empty[acc], 0);
-                else mbar_arrive(&acc_empty[acc]);
-            }
+            if (lane == 0) mbar_arrive(rank == 0 ? &acc_empty[acc] : &acc_read[acc]);
         }
     }
 

@@ -140,6 +140,18 @@ __device__ __forceinline__ void tma_load_3d_cg(void* dst, const CUtensorMap* map
             : "memory");
 }
 
+// 16 lanes x 32 consecutive 32-bit columns as four 16 x 8 fragments: registers 4 i, 4 i + 1 of
+// thread t hold lane t / 4, columns 8 i + 2 (t % 4) and the next, 4 i + 2 and 4 i + 3 lane t / 4 + 8.
+__device__ __forceinline__ void tc_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 // ------------------------------------------------------------------ commits
 
 // Arrive on the barrier (of both CTAs of the pair, at the same address) once every tcgen05

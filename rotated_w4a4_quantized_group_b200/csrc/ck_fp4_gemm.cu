@@ -11,9 +11,9 @@
 // its 128 lanes.  CG = 2: two CTAs of a cluster form one 256 x BN tile with
 // tcgen05.mma.cta_group::2; each holds its own 128 channels and half of the rows' codes, so a
 // byte of shared memory feeds twice the math.  Per stage of 256 k (four MMAs):
-//   warp 0   TMA of the weights' and rows' codes (128-byte rows, 128-byte swizzle) and of their
-//            scale tiles; the weights' part of the first stages before the wait for the kernel
-//            before this one (the quantizer)
+//   warps 0, 2, 3  TMA of the weights' codes, of the rows' codes (128-byte rows, 128-byte swizzle)
+//            and of both scale tiles; the weights' codes of the first stages before the wait for the
+//            kernel before this one (the quantizer)
 //   warp 1   copies the scale tiles from shared to tensor memory (tcgen05.cp, in order with the
 //            MMAs that read them) and issues the MMAs: the CTA of rank 0 for both CTAs
 //   warps 4-11  the epilogue: two warps per lane quarter on alternate 32-row chunks, from one of
@@ -37,7 +37,7 @@ namespace fp4g {
 constexpr int BW = 128;                 // channels per CTA
 constexpr int BK = 256;                 // k per stage: 128 bytes of codes
 constexpr int BN_MAX = 192;
-constexpr int WARP_TMA = 0, WARP_MMA = 1, EPI_WARP0 = 4, EPI_WARPS = 8;
+constexpr int WARP_TMA_W = 0, WARP_MMA = 1, WARP_TMA_X = 2, WARP_TMA_S = 3, EPI_WARP0 = 4, EPI_WARPS = 8;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 constexpr int STAGES_MAX = 8;
 constexpr uint32_t A_BYTES = BW * BK / 2;
@@ -70,7 +70,7 @@ struct Fp4GemmParams {
     int tiles_n;          // tiles along the channels
     int stages;
     uint32_t b_bytes;     // a CTA's codes of the rows per stage
-    uint32_t sfa_bytes, sfb_bytes, stage_bytes;
+    uint32_t stage_bytes;
     uint32_t idesc;
     int n_experts;        // 1 without offsets
     int n_sf_blocks;      // scale blocks of one weight matrix
@@ -195,7 +195,7 @@ __device__ __forceinline__ void epilogue_any(uint32_t taddr, float alpha, float 
     }
 }
 
-template <typename OutT, bool NV, int CG>
+template <typename OutT, bool NV, int CG, int NBLK>
 __global__ void __launch_bounds__(fp4g::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap xmap,
                     const __grid_constant__ CUtensorMap wmap,
@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
                     const __grid_constant__ CUtensorMap wsmap, Fp4GemmParams p) {
     using namespace fp4g;
     constexpr int SF_TILES = NV ? 4 : 2;     // scale tiles per stage and 128 rows
+    constexpr uint32_t SFA_BYTES = SF_TILES * kFp4TileBytes, SFB_BYTES = NBLK * SFA_BYTES;
     extern __shared__ __align__(1024) unsigned char fp4_smem[];
     unsigned char* ring = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(fp4_smem) + 1023) & ~uintptr_t(1023));
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     __shared__ uint32_t commits[2];          // rank 0's count of stage and of accumulator commits
-    __shared__ uint32_t loaded;              // stages whose loads this CTA issued
+    __shared__ uint32_t loaded[3];           // stages whose loads this CTA's producers issued
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
 
     if (tid == 0) {
         for (int s = 0; s < STAGES_MAX; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 3);
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
         }
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
-        commits[0] = commits[1] = loaded = 0;
+        commits[0] = commits[1] = loaded[0] = loaded[1] = loaded[2] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&xmap);
         tma_prefetch_desc(&wmap);
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
         tmem_relinquish_cg<CG>();
     }
     // tiles before each expert's: a running sum over the experts, 32 at a time
-    if (warp == 2) {
+    if (warp == EPI_WARP0) {
         int before = 0;
         for (int e0 = 0; e0 < p.n_experts; e0 += 32) {
             const int e = e0 + lane;
@@ -276,76 +277,71 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     const uint32_t tmem_base = tmem_base_sh;
     const int tiles = cum[p.n_experts];
     const uint32_t num_kb = (uint32_t)p.num_kb;
-    const uint32_t load_bytes = A_BYTES + p.b_bytes + p.sfa_bytes + p.sfb_bytes;   // a CTA's, a stage
+    // bytes of a stage that a producer of one CTA loads
+    auto part_bytes = [&](int part) { return part == 0 ? A_BYTES : part == 1 ? p.b_bytes : SFA_BYTES + SFB_BYTES; };
     const uint32_t full0 = CG == 2 ? cluster_address(&full[0], 0) : smem_u32(&full[0]);
     const uint32_t my_tiles = tiles > unit ? (uint32_t)((tiles - unit + units - 1) / units) : 0u;
     const uint32_t my_stages = my_tiles * num_kb;
 
-    if (warp == WARP_TMA) {
+    if (warp == WARP_TMA_W || warp == WARP_TMA_X || warp == WARP_TMA_S) {
         // ---------------------------------------------------------------- loads
-        // both CTAs' copies of a stage complete on rank 0's barrier, which rank 0 arms for both
-        if (lane == 0) {
-            uint32_t issued = 0;
-            auto load_w = [&](const Fp4Tile& t, uint32_t kb, uint32_t s) {
-                unsigned char* st = ring + (size_t)s * p.stage_bytes;
-                const uint32_t bar = full0 + s * 8;
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * load_bytes);
-                tma_load_3d_cg<CG>(st, &wmap, bar, (int32_t)(kb * (BK / 2)),
-                                   (int32_t)t.n0 + (int32_t)rank * BW, t.e);
-                tma_load_3d_cg<CG>(st + A_BYTES + p.b_bytes, &wsmap, bar, 0, (int32_t)(kb * SF_TILES),
-                                   t.e * p.n_sf_blocks + (int)(t.n0 / BW) + (int)rank);
-            };
-            auto load_x = [&](const Fp4Tile& t, uint32_t kb, uint32_t s) {
-                unsigned char* st = ring + (size_t)s * p.stage_bytes;
-                const uint32_t bar = full0 + s * 8;
-                tma_load_2d_cg<CG>(st + A_BYTES, &xmap, bar, (int32_t)(kb * (BK / 2)),
-                                   (int32_t)t.m0 + (int32_t)rank * (p.BN / CG));
-                tma_load_3d_cg<CG>(st + A_BYTES + p.b_bytes + p.sfa_bytes, &xsmap, bar, 0,
-                                   (int32_t)(kb * SF_TILES), t.sf_block);
-            };
-            // the weights of the first stages, then the rows once the kernel before has written them
-            const uint32_t head = my_stages < S ? my_stages : S;
-            Fp4Tile t = {};
-            uint32_t kb = 0, lt = 0;
-            for (uint32_t i = 0; i < head; ++i) {
-                if (kb == 0) t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
-                load_w(t, kb, i);
-                if (++kb == num_kb) {
-                    kb = 0;
-                    ++lt;
+        // Three warps issue a stage's boxes at once: the weights' codes, the rows' codes, and both
+        // scales (issuing is what one warp alone would be bound by: about 170 cycles a box).  Both
+        // CTAs' copies of a stage complete on rank 0's barrier, which rank 0 arms for both.  The
+        // whole warp walks the ring, so that the operands are uniform; one elected lane issues.
+        const bool leader = elect_one();
+        const int part = warp == WARP_TMA_W ? 0 : warp == WARP_TMA_X ? 1 : 2;
+        const uint32_t bytes = part_bytes(part);
+        // the weights' codes of the first stages do not wait for the kernel before this one
+        if (part != 0) grid_dependency_wait();
+        uint32_t s = 0, phase = 0, issued = 0;
+        bool ok = true;
+        for (uint32_t lt = 0; ok && lt < my_tiles; ++lt) {
+            const Fp4Tile t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
+            const int32_t w_row = (int32_t)t.n0 + (int32_t)rank * BW;
+            const int32_t w_sf = t.e * p.n_sf_blocks + (int)(t.n0 / BW) + (int)rank;
+            const int32_t x_row = (int32_t)t.m0 + (int32_t)rank * (p.BN / CG);
+            for (uint32_t kb = 0; kb < num_kb; ++kb) {
+                if (issued >= S) {
+                    // this wait covers MMAs that need the rows: it starts after the kernel before
+                    if (part == 0 && issued == S) grid_dependency_wait();
+                    if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], phase ^ 1u, &abort_flag, p.dev_status))) {
+                        ok = false;
+                        break;
+                    }
                 }
-            }
-            grid_dependency_wait();
-            kb = lt = 0;
-            uint32_t s = 0, phase = 0;
-            for (uint32_t i = 0; i < my_stages; ++i) {
-                if (kb == 0) t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
-                if (i >= head) {
-                    if (!mbar_wait(&empty[s], phase ^ 1u, &abort_flag, p.dev_status)) break;
-                    load_w(t, kb, s);
+                if (leader) {
+                    unsigned char* st = ring + (size_t)s * p.stage_bytes;
+                    const uint32_t bar = full0 + s * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * bytes);
+                    if (part == 0) {
+                        tma_load_3d_cg<CG>(st, &wmap, bar, (int32_t)(kb * (BK / 2)), w_row, t.e);
+                    } else if (part == 1) {
+                        tma_load_2d_cg<CG>(st + A_BYTES, &xmap, bar, (int32_t)(kb * (BK / 2)), x_row);
+                    } else {
+                        unsigned char* sf = st + A_BYTES + p.b_bytes;
+                        tma_load_3d_cg<CG>(sf, &wsmap, bar, 0, (int32_t)(kb * SF_TILES), w_sf);
+                        tma_load_3d_cg<CG>(sf + SFA_BYTES, &xsmap, bar, 0, (int32_t)(kb * SF_TILES), t.sf_block);
+                    }
                 }
-                load_x(t, kb, s);
+                __syncwarp();
                 ++issued;
-                if (++kb == num_kb) {
-                    kb = 0;
-                    ++lt;
-                }
                 if (++s == S) {
                     s = 0;
                     phase ^= 1u;
                 }
             }
-            // the weights' part of a head stage is in flight even where its rows' part is not: the
-            // loop above issues every head stage's, as nothing makes it stop before
-            loaded = issued;
         }
+        if (leader) loaded[part] = issued;
         __syncwarp();
     } else if (warp == WARP_MMA && rank == 0) {
         // ---------------------------------------------------------------- MMA issuer
         // the whole warp takes every wait and computes every operand; one elected lane issues
         grid_dependency_wait();
         const bool leader = elect_one();
-        const uint32_t ring_u = smem_u32(ring);
+        // descriptors of stage 0; a stage is stage_bytes further (addresses count 16-byte units)
+        const uint64_t a_desc0 = smem_desc_k_sw128(smem_u32(ring));
+        const uint64_t sf_desc0 = smem_desc_scales(smem_u32(ring) + A_BYTES + p.b_bytes);
         uint32_t s = 0, phase = 0, n_stage = 0, n_acc = 0;
         bool ok = true;
         for (uint32_t lt = 0; ok && lt < my_tiles; ++lt) {
@@ -362,29 +358,32 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t st = ring_u + s * p.stage_bytes;
                 const uint32_t sfa = tmem_base + SF_COL + (n_stage & 1u) * SF_SET;
                 const uint32_t sfb = sfa + 16;
                 const uint32_t left = (uint32_t)p.k64 - kb * 4;
                 const uint32_t steps = left < 4 ? left : 4;
                 if (leader) {
-                    const uint64_t sa = smem_desc_scales(st + A_BYTES + p.b_bytes);
-                    const uint64_t sb = smem_desc_scales(st + A_BYTES + p.b_bytes + p.sfa_bytes);
+                    const uint64_t sa = sf_desc0 + (uint64_t)(s * (p.stage_bytes >> 4));
+                    const uint64_t sb = sa + (SFA_BYTES >> 4);
 #pragma unroll
                     for (int j = 0; j < SF_TILES; ++j) {
                         tc_cp_scales<CG>(sfa + 4 * j, sa + (uint64_t)(j * (kFp4TileBytes >> 4)));
-                        tc_cp_scales<CG>(sfb + 4 * j * p.nblk, sb + (uint64_t)(j * (kFp4TileBytes >> 4)));
-                        if (p.nblk == 2)
-                            tc_cp_scales<CG>(sfb + 8 * j + 4,
-                                             sb + (uint64_t)((SF_TILES + j) * (kFp4TileBytes >> 4)));
+#pragma unroll
+                        for (int b = 0; b < NBLK; ++b)
+                            tc_cp_scales<CG>(sfb + 4 * (NBLK * j + b),
+                                             sb + (uint64_t)((b * SF_TILES + j) * (kFp4TileBytes >> 4)));
                     }
-                    const uint64_t ad = smem_desc_k_sw128(st), bd = smem_desc_k_sw128(st + A_BYTES);
-                    for (uint32_t j = 0; j < steps; ++j) {
-                        // MX: a tile holds the scales of two steps, bytes 0-1 and 2-3 of a word
-                        const uint32_t tile = NV ? j : j >> 1, half = NV ? 0u : (j & 1u) * 2u;
-                        tc_mma_fp4<NV, CG>(d, ad + (uint64_t)(j * 2), bd + (uint64_t)(j * 2),
-                                           p.idesc | (half << 4) | (half << 29), sfa + 4 * tile,
-                                           sfb + 4 * tile * p.nblk + t.sf_shift, (kb | j) != 0 ? 1u : 0u);
+                    const uint64_t ad = a_desc0 + (uint64_t)(s * (p.stage_bytes >> 4));
+                    const uint64_t bd = ad + (A_BYTES >> 4);
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j) {
+                        if (j < steps) {
+                            // MX: a tile holds the scales of two steps, bytes 0-1 and 2-3 of a word
+                            const uint32_t tile = NV ? j : j >> 1, half = NV ? 0u : (j & 1u) * 2u;
+                            tc_mma_fp4<NV, CG>(d, ad + (uint64_t)(j * 2), bd + (uint64_t)(j * 2),
+                                               p.idesc | (half << 4) | (half << 29), sfa + 4 * tile,
+                                               sfb + 4 * NBLK * tile + t.sf_shift, (kb | j) != 0 ? 1u : 0u);
+                        }
                     }
                     tc_commit_cg<CG>(&empty[s]);
                     if (kb + 1 == num_kb) tc_commit_cg<CG>(&acc_full[acc]);
@@ -460,13 +459,21 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     if (CG == 2) cluster_sync_all();   // rank 0's MMAs have completed, and the counts are readable
     if (tid == 0) {
         if (rank == 0) {
-            // every copy has landed: where only one CTA issued a stage's (after a timeout), the
-            // barrier is told so
-            const uint32_t mine = loaded, other = CG == 2 ? dsmem_load_u32(&loaded, 1) : mine;
-            const uint32_t n = mine > other ? mine : other;
+            // every copy has landed: what a producer did not issue of a stage that another did (after
+            // a timeout) its barrier is told not to expect
+            uint32_t n = 0;
+            for (int part = 0; part < 3; ++part) {
+                n = max(n, loaded[part]);
+                if (CG == 2) n = max(n, dsmem_load_u32(&loaded[part], 1));
+            }
             for (uint32_t j = n > S ? n - S : 0; j < n; ++j) {
-                if (j >= mine) mbar_arrive_expect_tx(&full[j % S], load_bytes);
-                else if (j >= other) mbar_complete_tx(&full[j % S], load_bytes);
+                for (int part = 0; part < 3; ++part) {
+                    const bool mine = j < loaded[part];
+                    const bool other = CG == 2 ? j < dsmem_load_u32(&loaded[part], 1) : mine;
+                    if (!mine && other) mbar_arrive_expect_tx(&full[j % S], part_bytes(part));
+                    else if (!mine) mbar_arrive(&full[j % S]);
+                    else if (!other) mbar_complete_tx(&full[j % S], part_bytes(part));
+                }
                 mbar_wait(&full[j % S], (j / S) & 1u, nullptr, p.dev_status);
             }
         }
@@ -520,10 +527,10 @@ static Fp4Shape choose_shape(int64_t M, int64_t N, int64_t num_kb, int n_experts
     return best;
 }
 
-template <typename OutT, bool NV, int CG>
+template <typename OutT, bool NV, int CG, int NBLK>
 static ck_status fp4_launch(const CUtensorMap* maps, const Fp4GemmParams& p, size_t smem, int grid,
                             bool dep, cudaStream_t stream) {
-    auto kern = fp4_gemm_kernel<OutT, NV, CG>;
+    auto kern = fp4_gemm_kernel<OutT, NV, CG, NBLK>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return CK_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -555,11 +562,14 @@ static ck_status fp4_launch(const CUtensorMap* maps, const Fp4GemmParams& p, siz
 template <typename OutT>
 static ck_status fp4_launch_out(const CUtensorMap* maps, const Fp4GemmParams& p, size_t smem, int grid,
                                 bool nv, int cg, bool dep, cudaStream_t stream) {
+    const bool two = p.nblk == 2;   // BN = 192, which only pairs take
     if (nv)
-        return cg == 2 ? fp4_launch<OutT, true, 2>(maps, p, smem, grid, dep, stream)
-                       : fp4_launch<OutT, true, 1>(maps, p, smem, grid, dep, stream);
-    return cg == 2 ? fp4_launch<OutT, false, 2>(maps, p, smem, grid, dep, stream)
-                   : fp4_launch<OutT, false, 1>(maps, p, smem, grid, dep, stream);
+        return cg == 1 ? fp4_launch<OutT, true, 1, 1>(maps, p, smem, grid, dep, stream)
+               : two   ? fp4_launch<OutT, true, 2, 2>(maps, p, smem, grid, dep, stream)
+                       : fp4_launch<OutT, true, 2, 1>(maps, p, smem, grid, dep, stream);
+    return cg == 1 ? fp4_launch<OutT, false, 1, 1>(maps, p, smem, grid, dep, stream)
+           : two   ? fp4_launch<OutT, false, 2, 2>(maps, p, smem, grid, dep, stream)
+                   : fp4_launch<OutT, false, 2, 1>(maps, p, smem, grid, dep, stream);
 }
 
 ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream) {
@@ -580,9 +590,8 @@ ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream) {
     // the tile count stays an int: rows split over experts give at most one more tile each
     if ((double)p.tiles_n * ((double)a.M / p.BN + E + 1) >= 2147483647.0) return CK_ERR_UNSUPPORTED;
     p.b_bytes = (uint32_t)(shape.bn / shape.cg) * (BK / 2);
-    p.sfa_bytes = (a.nv ? 4 : 2) * kFp4TileBytes;
-    p.sfb_bytes = p.sfa_bytes * p.nblk;
-    p.stage_bytes = (A_BYTES + p.b_bytes + p.sfa_bytes + p.sfb_bytes + 1023) & ~1023u;
+    const uint32_t sf_bytes = (a.nv ? 4 : 2) * kFp4TileBytes * (1 + p.nblk);
+    p.stage_bytes = (A_BYTES + p.b_bytes + sf_bytes + 1023) & ~1023u;
     const size_t fixed = 1024 + EPI_WARPS * EPI_STAGE_BYTES + (size_t)(E + 1) * sizeof(int);
     p.stages = (int)((SMEM_MAX - fixed) / p.stage_bytes);
     if (p.stages > STAGES_MAX) p.stages = STAGES_MAX;

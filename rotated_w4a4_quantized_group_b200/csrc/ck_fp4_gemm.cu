@@ -281,36 +281,33 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     auto part_bytes = [&](int part) { return part == 0 ? A_BYTES : part == 1 ? p.b_bytes : SFA_BYTES + SFB_BYTES; };
     const uint32_t full0 = CG == 2 ? cluster_address(&full[0], 0) : smem_u32(&full[0]);
     const uint32_t my_tiles = tiles > unit ? (uint32_t)((tiles - unit + units - 1) / units) : 0u;
-    const uint32_t my_stages = my_tiles * num_kb;
 
     if (warp == WARP_TMA_W || warp == WARP_TMA_X || warp == WARP_TMA_S) {
         // ---------------------------------------------------------------- loads
         // Three warps issue a stage's boxes at once: the weights' codes, the rows' codes, and both
-        // scales (issuing is what one warp alone would be bound by: about 170 cycles a box).  Both
-        // CTAs' copies of a stage complete on rank 0's barrier, which rank 0 arms for both.  The
-        // whole warp walks the ring, so that the operands are uniform; one elected lane issues.
-        const bool leader = elect_one();
-        const int part = warp == WARP_TMA_W ? 0 : warp == WARP_TMA_X ? 1 : 2;
-        const uint32_t bytes = part_bytes(part);
-        // the weights' codes of the first stages do not wait for the kernel before this one
-        if (part != 0) grid_dependency_wait();
-        uint32_t s = 0, phase = 0, issued = 0;
-        bool ok = true;
-        for (uint32_t lt = 0; ok && lt < my_tiles; ++lt) {
-            const Fp4Tile t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
-            const int32_t w_row = (int32_t)t.n0 + (int32_t)rank * BW;
-            const int32_t w_sf = t.e * p.n_sf_blocks + (int)(t.n0 / BW) + (int)rank;
-            const int32_t x_row = (int32_t)t.m0 + (int32_t)rank * (p.BN / CG);
-            for (uint32_t kb = 0; kb < num_kb; ++kb) {
-                if (issued >= S) {
-                    // this wait covers MMAs that need the rows: it starts after the kernel before
-                    if (part == 0 && issued == S) grid_dependency_wait();
-                    if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], phase ^ 1u, &abort_flag, p.dev_status))) {
-                        ok = false;
-                        break;
+        // scales (one warp alone is bound by issuing them: about 170 cycles a box).  Both CTAs'
+        // copies of a stage complete on rank 0's barrier, which rank 0 arms for both.
+        if (elect_one()) {
+            const int part = warp == WARP_TMA_W ? 0 : warp == WARP_TMA_X ? 1 : 2;
+            const uint32_t bytes = part_bytes(part);
+            // the weights' codes of the first stages do not wait for the kernel before this one
+            if (part != 0) grid_dependency_wait();
+            uint32_t s = 0, phase = 0, issued = 0;
+            bool ok = true;
+            for (uint32_t lt = 0; ok && lt < my_tiles; ++lt) {
+                const Fp4Tile t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
+                const int32_t w_row = (int32_t)t.n0 + (int32_t)rank * BW;
+                const int32_t w_sf = t.e * p.n_sf_blocks + (int)(t.n0 / BW) + (int)rank;
+                const int32_t x_row = (int32_t)t.m0 + (int32_t)rank * (p.BN / CG);
+                for (uint32_t kb = 0; kb < num_kb; ++kb) {
+                    if (issued >= S) {
+                        // this wait covers MMAs that need the rows: it starts after the kernel before
+                        if (part == 0 && issued == S) grid_dependency_wait();
+                        if (!mbar_wait(&empty[s], phase ^ 1u, &abort_flag, p.dev_status)) {
+                            ok = false;
+                            break;
+                        }
                     }
-                }
-                if (leader) {
                     unsigned char* st = ring + (size_t)s * p.stage_bytes;
                     const uint32_t bar = full0 + s * 8;
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * bytes);
@@ -323,82 +320,88 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
                         tma_load_3d_cg<CG>(sf, &wsmap, bar, 0, (int32_t)(kb * SF_TILES), w_sf);
                         tma_load_3d_cg<CG>(sf + SFA_BYTES, &xsmap, bar, 0, (int32_t)(kb * SF_TILES), t.sf_block);
                     }
-                }
-                __syncwarp();
-                ++issued;
-                if (++s == S) {
-                    s = 0;
-                    phase ^= 1u;
+                    ++issued;
+                    if (++s == S) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
+            loaded[part] = issued;
         }
-        if (leader) loaded[part] = issued;
         __syncwarp();
     } else if (warp == WARP_MMA && rank == 0) {
         // ---------------------------------------------------------------- MMA issuer
-        // the whole warp takes every wait and computes every operand; one elected lane issues
-        grid_dependency_wait();
-        const bool leader = elect_one();
-        // descriptors of stage 0; a stage is stage_bytes further (addresses count 16-byte units)
-        const uint64_t a_desc0 = smem_desc_k_sw128(smem_u32(ring));
-        const uint64_t sf_desc0 = smem_desc_scales(smem_u32(ring) + A_BYTES + p.b_bytes);
-        uint32_t s = 0, phase = 0, n_stage = 0, n_acc = 0;
-        bool ok = true;
-        for (uint32_t lt = 0; ok && lt < my_tiles; ++lt) {
-            const Fp4Tile t = fp4_tile<CG>(p, cum, unit + (int)lt * units);
-            const uint32_t acc = lt & 1u;
-            if (lt >= 2 && !__all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], ((lt >> 1) - 1) & 1u,
-                                                                      &abort_flag, p.dev_status)))
-                break;
-            tc_fence_after();
-            const uint32_t d = tmem_base + acc * BN_MAX;
-            for (uint32_t kb = 0; kb < num_kb; ++kb) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, &abort_flag, p.dev_status))) {
-                    ok = false;
+        // One elected thread walks the ring.  What it executes per stage is what bounds large
+        // products, so the loop only adds to the low words of its descriptors.
+        if (elect_one()) {
+            grid_dependency_wait();
+            const uint32_t slot_step = p.stage_bytes >> 4;   // descriptors count 16-byte units
+            const uint64_t ab = smem_desc_k_sw128(smem_u32(ring));
+            const uint64_t sf = smem_desc_scales(smem_u32(ring) + A_BYTES + p.b_bytes);
+            const uint32_t ab_hi = (uint32_t)(ab >> 32), sf_hi = (uint32_t)(sf >> 32);
+            uint32_t ab_lo = (uint32_t)ab, sf_lo = (uint32_t)sf;
+            uint32_t s = 0, phase = 0, n_stage = 0, n_acc = 0;
+            bool ok = true;
+            for (uint32_t lt = 0; ok && lt < my_tiles; ++lt) {
+                const uint32_t shift = (uint32_t)fp4_tile<CG>(p, cum, unit + (int)lt * units).sf_shift;
+                const uint32_t acc = lt & 1u;
+                if (lt >= 2 && !mbar_wait_cluster(&acc_empty[acc], ((lt >> 1) - 1) & 1u, &abort_flag, p.dev_status))
                     break;
-                }
                 tc_fence_after();
-                const uint32_t sfa = tmem_base + SF_COL + (n_stage & 1u) * SF_SET;
-                const uint32_t sfb = sfa + 16;
-                const uint32_t left = (uint32_t)p.k64 - kb * 4;
-                const uint32_t steps = left < 4 ? left : 4;
-                if (leader) {
-                    const uint64_t sa = sf_desc0 + (uint64_t)(s * (p.stage_bytes >> 4));
-                    const uint64_t sb = sa + (SFA_BYTES >> 4);
+                const uint32_t d = tmem_base + acc * BN_MAX;
+#pragma unroll 2
+                for (uint32_t kb = 0; kb < num_kb; ++kb) {
+                    if (!mbar_wait(&full[s], phase, &abort_flag, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sfa = tmem_base + SF_COL + (n_stage & 1u) * SF_SET;
+                    const uint32_t sfb = sfa + 16;
 #pragma unroll
                     for (int j = 0; j < SF_TILES; ++j) {
-                        tc_cp_scales<CG>(sfa + 4 * j, sa + (uint64_t)(j * (kFp4TileBytes >> 4)));
+                        tc_cp_scales<CG>(sfa + 4 * j, sf_lo + j * (kFp4TileBytes >> 4), sf_hi);
 #pragma unroll
                         for (int b = 0; b < NBLK; ++b)
                             tc_cp_scales<CG>(sfb + 4 * (NBLK * j + b),
-                                             sb + (uint64_t)((b * SF_TILES + j) * (kFp4TileBytes >> 4)));
+                                             sf_lo + (SFA_BYTES + (b * SF_TILES + j) * kFp4TileBytes) / 16, sf_hi);
                     }
-                    const uint64_t ad = a_desc0 + (uint64_t)(s * (p.stage_bytes >> 4));
-                    const uint64_t bd = ad + (A_BYTES >> 4);
-#pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j) {
-                        if (j < steps) {
-                            // MX: a tile holds the scales of two steps, bytes 0-1 and 2-3 of a word
-                            const uint32_t tile = NV ? j : j >> 1, half = NV ? 0u : (j & 1u) * 2u;
-                            tc_mma_fp4<NV, CG>(d, ad + (uint64_t)(j * 2), bd + (uint64_t)(j * 2),
-                                               p.idesc | (half << 4) | (half << 29), sfa + 4 * tile,
-                                               sfb + 4 * NBLK * tile + t.sf_shift, (kb | j) != 0 ? 1u : 0u);
-                        }
+                    // step j: 32 bytes further in the 128-byte rows.  MX: a scale tile holds two
+                    // steps, bytes 0-1 and 2-3 of a word
+                    auto step = [&](uint32_t j, uint32_t accumulate) {
+                        const uint32_t tile = NV ? j : j >> 1, half = NV ? 0u : (j & 1u) * 2u;
+                        tc_mma_fp4<NV, CG>(d, ab_lo + j * 2, ab_lo + j * 2 + (A_BYTES >> 4), ab_hi,
+                                           p.idesc | (half << 4) | (half << 29), sfa + 4 * tile,
+                                           sfb + 4 * NBLK * tile + shift, accumulate);
+                    };
+                    const uint32_t left = (uint32_t)p.k64 - kb * 4;
+                    step(0, kb != 0 ? 1u : 0u);
+                    if (left >= 4) {
+                        step(1, 1u);
+                        step(2, 1u);
+                        step(3, 1u);
+                    } else {
+                        if (left > 1) step(1, 1u);
+                        if (left > 2) step(2, 1u);
                     }
                     tc_commit_cg<CG>(&empty[s]);
-                    if (kb + 1 == num_kb) tc_commit_cg<CG>(&acc_full[acc]);
+                    ++n_stage;
+                    ab_lo += slot_step;
+                    sf_lo += slot_step;
+                    if (++s == S) {
+                        s = 0;
+                        phase ^= 1u;
+                        ab_lo = (uint32_t)ab;
+                        sf_lo = (uint32_t)sf;
+                    }
                 }
-                __syncwarp();
-                ++n_stage;
-                if (kb + 1 == num_kb) ++n_acc;
-                if (++s == S) {
-                    s = 0;
-                    phase ^= 1u;
+                if (ok) {
+                    tc_commit_cg<CG>(&acc_full[acc]);
+                    ++n_acc;
                 }
             }
-        }
-        // every MMA and copy issued above has completed once drain_bar flips
-        if (leader) {
+            // every MMA and copy issued above has completed once drain_bar flips
             tc_commit_local<CG>(&drain_bar);
             mbar_wait(&drain_bar, 0, nullptr, p.dev_status);
             commits[0] = n_stage;

@@ -194,11 +194,18 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
 
 // One scale tile into four tensor-memory columns: word 4 i + j of the tile goes to lane i, column j
 // of each of the four lane quarters (of both CTAs, each from its own shared memory, for CG = 2).
-template <int CG> __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t sdesc) {
-    if (CG == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+template <int CG>
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t desc_lo, uint32_t desc_hi) {
+#define CK_FP4_CP(group)                                                             \
+    asm volatile(                                                                    \
+        "{\n\t.reg .b64 s;\n\t"                                                     \
+        "mov.b64 s, {%1, %2};\n\t"                                                   \
+        "tcgen05.cp.cta_group::" group ".32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr), \
+        "r"(desc_lo), "r"(desc_hi)                                                   \
+        : "memory")
+    if (CG == 1) CK_FP4_CP("1");
+    else CK_FP4_CP("2");
+#undef CK_FP4_CP
 }
 
 // Instruction descriptor of tcgen05.mma kind::mxf4nvf4: E2M1 A and B, both K-major, M x N (M over
@@ -211,17 +218,20 @@ __host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool nv) {
 
 // D[tmem] (+)= A[smem] * B[smem]^T over 64 k, each product times A's and B's block scales in
 // tensor memory: one scale byte per 16 k (NV, four to a word) or 32 k (MX, two to a word).
+// The descriptors of A and B share their high word.
 template <bool NV, int CG>
-__device__ __forceinline__ void tc_mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+__device__ __forceinline__ void tc_mma_fp4(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t ab_hi,
                                            uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                            uint32_t accumulate) {
 #define CK_FP4_MMA(group, vec)                                                                     \
     asm volatile(                                                                                  \
-        "{\n\t.reg .pred p;\n\t"                                                                   \
-        "setp.ne.b32 p, %6, 0;\n\t"                                                                \
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"                                               \
+        "setp.ne.b32 p, %7, 0;\n\t"                                                                \
+        "mov.b64 a, {%1, %3};\n\t"                                                                 \
+        "mov.b64 b, {%2, %3};\n\t"                                                                 \
         "tcgen05.mma.cta_group::" group ".kind::mxf4nvf4.block_scale.scale_vec::" vec              \
-        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),                                    \
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                  \
+        " [%0], a, b, %4, [%5], [%6], p;\n\t}" ::"r"(d_tmem),                                      \
+        "r"(a_lo), "r"(b_lo), "r"(ab_hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)          \
         : "memory")
     if (NV) {
         if (CG == 1) CK_FP4_MMA("1", "4X");

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     __shared__ uint32_t commits[2];          // rank 0's count of stage and of accumulator commits
-    __shared__ uint32_t loaded[3];           // stages whose loads this CTA's producers issued
+    __shared__ uint32_t loaded[2][3];        // stages whose loads each CTA's producers issued
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
         }
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
-        commits[0] = commits[1] = loaded[0] = loaded[1] = loaded[2] = 0;
+        commits[0] = commits[1] = 0;
+        for (int i = 0; i < 6; ++i) loaded[i / 3][i % 3] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&xmap);
         tma_prefetch_desc(&wmap);
@@ -327,7 +328,8 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
                     }
                 }
             }
-            loaded[part] = issued;
+            loaded[rank][part] = issued;
+            if (rank != 0) dsmem_store_u32(&loaded[1][part], 0, issued);
         }
         __syncwarp();
     } else if (warp == WARP_MMA && rank == 0) {
@@ -406,6 +408,10 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
             mbar_wait(&drain_bar, 0, nullptr, p.dev_status);
             commits[0] = n_stage;
             commits[1] = n_acc;
+            if (CG == 2) {
+                dsmem_store_u32(&commits[0], 1, n_stage);
+                dsmem_store_u32(&commits[1], 1, n_acc);
+            }
         }
         __syncwarp();
     } else if (CG == 2 && warp == WARP_MMA) {
@@ -459,20 +465,16 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();   // rank 0's MMAs have completed, and the counts are readable
+    if (CG == 2) cluster_sync_all();   // rank 0's MMAs have completed, and the counts are there
     if (tid == 0) {
         if (rank == 0) {
             // every copy has landed: what a producer did not issue of a stage that another did (after
             // a timeout) its barrier is told not to expect
             uint32_t n = 0;
-            for (int part = 0; part < 3; ++part) {
-                n = max(n, loaded[part]);
-                if (CG == 2) n = max(n, dsmem_load_u32(&loaded[part], 1));
-            }
+            for (int i = 0; i < 3 * CG; ++i) n = max(n, loaded[i / 3][i % 3]);
             for (uint32_t j = n > S ? n - S : 0; j < n; ++j) {
                 for (int part = 0; part < 3; ++part) {
-                    const bool mine = j < loaded[part];
-                    const bool other = CG == 2 ? j < dsmem_load_u32(&loaded[part], 1) : mine;
+                    const bool mine = j < loaded[0][part], other = CG == 2 ? j < loaded[1][part] : mine;
                     if (!mine && other) mbar_arrive_expect_tx(&full[j % S], part_bytes(part));
                     else if (!mine) mbar_arrive(&full[j % S]);
                     else if (!other) mbar_complete_tx(&full[j % S], part_bytes(part));
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
         }
         if (CG == 2) {
             // the arrivals of rank 0's commits at this CTA's barriers have come
-            const uint32_t n = dsmem_load_u32(&commits[0], 0), a = dsmem_load_u32(&commits[1], 0);
+            const uint32_t n = commits[0], a = commits[1];
             for (uint32_t j = n > S ? n - S : 0; j < n; ++j)
                 mbar_wait(&empty[j % S], (j / S) & 1u, nullptr, p.dev_status);
             for (uint32_t j = a > 2 ? a - 2 : 0; j < a; ++j)

@@ -64,6 +64,11 @@ __device__ __forceinline__ uint32_t cluster_address(const void* local, uint32_t 
     return remote;
 }
 
+// A word of CTA `rank`'s shared memory at the address of `local` in this CTA.
+__device__ __forceinline__ void dsmem_store_u32(void* local, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_address(local, rank)), "r"(v) : "memory");
+}
+
 // Account for bytes that no copy will bring.
 __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)

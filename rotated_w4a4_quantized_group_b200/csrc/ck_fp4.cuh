@@ -115,21 +115,16 @@ __device__ __forceinline__ float odd_from_rn(float q, float a, float b) {
     return __uint_as_float(u);
 }
 
-// The E4M3 byte of amax / c (c = fl(6 t)), rounded from the exact quotient.
-__device__ __forceinline__ uint32_t nv_scale_byte(float amax, float c) {
-    if (c < 0x1p-60f) {   // far from the subnormal range; an overflow of amax saturates as it should
-        amax = __fmul_rn(amax, 0x1p64f);
-        c = __fmul_rn(c, 0x1p64f);
-    }
-    // below 2^-60 / 2^40 the quotient rounds to zero whatever the remainder's last bits say
-    float q = __fdiv_rn(amax, c);
-    if (q < 1024.0f && amax > 0x1p-100f) q = odd_from_rn(q, amax, c);
-    return e4m3_byte(q);
+// 1 / d within one step, for d and 1 / d far from the subnormal range.
+__device__ __forceinline__ float reciprocal(float d) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return __fmaf_rn(__fmaf_rn(-d, r, 1.0f), r, r);
 }
 
 // Code of one value by comparing it with the borders times d, exactly (3-bit border times 24-bit
 // d in fp64): the path of blocks whose scale is too small or large for the fp32 quotient.
-static __device__ __noinline__ uint32_t fp4_code_exact(float x, float d) {
+__device__ __forceinline__ uint32_t fp4_code_exact(float x, float d) {
     const double a = fabs((double)x), s = (double)d;
     uint32_t n = 0;
     n += a > 0.25 * s;
@@ -142,83 +137,186 @@ static __device__ __noinline__ uint32_t fp4_code_exact(float x, float d) {
     return n | (__float_as_uint(x) >> 28 & 8u);
 }
 
+// The significant bits of a type's values below which an fp32 mantissa is zero.
+template <typename T> struct GridBits { static constexpr int value = 0; };          // fp32: none
+template <> struct GridBits<__nv_bfloat16> { static constexpr int value = 16; };
+template <> struct GridBits<__half> { static constexpr int value = 13; };
+
 // What the quantizer of a tensor keeps across its blocks.
 struct Fp4Tensor {
     float t;      // the tensor scale (NV)
-    float c;      // fl(6 t)
+    float c;      // fl(6 t), brought between 2^-83 and 2^64 by a power of two
+    float rc;     // 1 / c
+    float up;     // that power
     bool t_ok;    // a positive finite number; otherwise every scale is NaN
+    bool t_mid;   // far enough from the ends for every s t and its reciprocal to be normal
+    // bit i: blocks whose scale has mantissa 1 + i / 8 want their reciprocal larger, smaller, or the
+    // rounded quotient
+    uint32_t larger, smaller, quotient;
 };
+
+// The tensor's constants; every lane of the warp calls it.
+//
+// x * r, r within a step of 1 / d, d = fl(s t), rounds to the code of x / d for every x of a 16-bit
+// type but those on which a border (0.25 to 5; four mantissas) times d all but falls: with t an
+// absmax / 2688, the usual calibration, every third block has such a border.  They want r a little
+// larger (x above its border), a little smaller (below), or exact; which depends on the mantissas of
+// s, border and t alone, so a warp finds it once for all 8 x 4 pairs.  In steps of a mantissa: r, the
+// product and the border are off by less than 3 together, so eight decide every such x, and no value
+// further than 24 from its border is moved over it; the next value of the type is at least 2^12
+// steps away.
+template <typename T>
 __device__ __forceinline__ Fp4Tensor fp4_tensor(const float* tensor_scale) {
+    constexpr int GRID = GridBits<T>::value;
     Fp4Tensor p;
     p.t = tensor_scale ? __ldg(tensor_scale) : 1.0f;
-    p.c = __fmul_rn(6.0f, p.t);
     p.t_ok = p.t > 0.0f && p.t <= 3.40282347e38f;
+    p.t_mid = p.t >= 0x1p-50f && p.t <= 0x1p50f;
+    p.c = __fmul_rn(6.0f, p.t);
+    p.up = p.c < 0x1p-60f ? 0x1p64f : p.c > 0x1p60f ? 0x1p-64f : 1.0f;
+    p.c = __fmul_rn(p.c, p.up);
+    if (p.c > 3.40282347e38f) {   // fl(6 t) overflowed: every quotient is zero
+        p.up = 0.0f;
+        p.c = 1.0f;
+    }
+    p.rc = reciprocal(p.c);
+    p.larger = p.smaller = p.quotient = 0u;
+    if (GRID > 0 && tensor_scale) {
+        constexpr int mask = (1 << GRID) - 1;
+        const int lane = threadIdx.x & 31;
+        const float tm = __uint_as_float((__float_as_uint(p.t) & 0x007FFFFFu) | 0x3F800000u);
+        const float d = __fmul_rn(1.0f + 0.125f * (lane >> 2), tm), m = 1.0f + 0.25f * (lane & 3);
+        const int b = __float_as_int(__fmul_rn(d, m));
+        const int g = (b + (mask + 1) / 2) & ~mask;              // the type's value nearest to d m
+        const float e = __fmaf_rn(-m, d, __int_as_float(g));     // its side, exactly
+        const bool near = abs(g - b) <= 24;
+        const uint32_t up = __ballot_sync(0xffffffffu, near && e > 0.0f);
+        const uint32_t down = __ballot_sync(0xffffffffu, near && e < 0.0f);
+        const uint32_t on = __ballot_sync(0xffffffffu, near && e == 0.0f);
+        const int sh = 4 * (lane & 7);
+        const bool u = (up >> sh & 15u) != 0u, w = (down >> sh & 15u) != 0u;
+        const bool bad = (on >> sh & 15u) != 0u || (u && w);
+        p.larger = __ballot_sync(0xffffffffu, lane < 8 && u && !bad);
+        p.smaller = __ballot_sync(0xffffffffu, lane < 8 && w && !bad);
+        p.quotient = __ballot_sync(0xffffffffu, lane < 8 && bad);
+    }
     return p;
 }
 
-// Sixteen values of one block (a whole NV block, half an MX block) with the block's absmax given
-// as the bits of an fp32 number (above infinity's for a NaN) -> sixteen codes and the block's
-// scale byte.  HAS_T: a tensor scale other than one may be given.
+// The E4M3 byte of amax / fl(6 t), rounded from the exact quotient: the quotient rounded correctly by
+// its residual, then to odd.  Where amax was scaled down into the subnormal range, or is there, the
+// quotient is below 2^-11 and rounds to zero whatever its last bits say; where it overflows, it
+// saturates.
+__device__ __forceinline__ uint32_t nv_scale_byte(float amax, const Fp4Tensor& p) {
+    const float a = __fmul_rn(amax, p.up);
+    const float q0 = __fmul_rn(a, p.rc);
+    const float q = __fmaf_rn(__fmaf_rn(-q0, p.c, a), p.rc, q0);
+    return e4m3_byte(q0 < 1024.0f ? odd_from_rn(q, a, p.c) : 1024.0f);
+}
+
+// One block's scale: its byte, the factor or divisor of its elements, and how they are divided.
+struct Fp4Scale {
+    uint32_t byte;
+    float d, r;      // NV: x / d, r its reciprocal; MX: x * r
+    int mode;        // 0: x * r; 1: the rounded quotient; 2: by comparison; 3: every code is zero
+};
+
+// The scale of a block of type T's values, from its absmax as the bits of an fp32 number (above
+// infinity's for a NaN).  HAS_T: a tensor scale other than one may be given.
 //
 // MX: byte = max(exponent field - 2, 0); x 2^-(byte - 127) is exact, so the conversion's rounding
 //     is the only one.
-// NV: s = e4m3(amax / c), d = fl(s t), code = e2m1(x / d).  The quotient is the correctly rounded
-//     one (reciprocal, one residual, one correction: see RowDivisor).  Where d = s has four bits,
-//     a quotient that is not on a border between two codes is at least 2^-24 of it away, so its
-//     rounding to 24 bits never moves it onto one; d = fl(s t) has 24 bits, and there the quotient
-//     is rounded to odd.
-template <bool NV, bool HAS_T>
-__device__ __forceinline__ uint32_t fp4_quant16(const float (&x)[16], uint32_t amax_bits,
-                                                const Fp4Tensor& p, uint32_t (&codes)[2]) {
-    codes[0] = codes[1] = 0u;
+// NV: s = e4m3(amax / c), d = fl(s t), code = e2m1(x / d).  With d = s, of four bits, the quotient is
+//     rounded correctly (reciprocal, one residual, one correction: see RowDivisor): off a border it
+//     is at least 2^-24 of it away, so its rounding never moves it onto one.  d = fl(s t) has 24
+//     bits.  There 16-bit values take x * (1 / d), moved where a border falls next to one of them (see
+//     fp4_tensor), or else, as fp32 values do, the quotient rounded to odd.
+template <typename T, bool NV, bool HAS_T>
+__device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, const Fp4Tensor& p) {
+    constexpr int GRID = GridBits<T>::value;
+    Fp4Scale b;
+    const bool finite = amax_bits < 0x7F800000u;
     if (!NV) {
-        if (amax_bits >= 0x7F800000u) return 0xFFu;
-        const int byte = max((int)(amax_bits >> 23) - 2, 0);
-        // 2^(127 - byte): exponent field 254 - byte, in 2..254
-        const float r = __uint_as_float((uint32_t)(254 - byte) << 23);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(x[8 * h + i], r);
-            codes[h] = fp4_pack8(v);
-        }
-        return (uint32_t)byte;
+        b.byte = (uint32_t)max((int)(amax_bits >> 23) - 2, 0);
+        b.r = __uint_as_float((254u - b.byte) << 23);   // 2^(127 - byte): exponent field 2 to 254
+        b.d = 0.0f;
+        b.mode = finite ? 0 : 3;
+        if (!finite) b.byte = 0xFFu;
+        return b;
     }
-    if (amax_bits >= 0x7F800000u || (HAS_T && !p.t_ok)) return 0x7Fu;
     const float amax = __uint_as_float(amax_bits);
-    const uint32_t byte = nv_scale_byte(amax, p.c);
-    const float s = e4m3_value(byte);
-    const float d = HAS_T ? __fmul_rn(s, p.t) : s;
-    if (d == 0.0f) return byte;
-    if (d >= 0x1p-60f && d <= 0x1p60f && amax <= 16.0f * d) {
-        const float r = __frcp_rn(d);
+    b.byte = nv_scale_byte(amax, p);
+    const float s = e4m3_value(b.byte);
+    b.d = HAS_T ? __fmul_rn(s, p.t) : s;
+    b.r = reciprocal(b.d);
+    if (HAS_T && GRID > 0) {
+        const uint32_t i = __float_as_uint(s) >> 20 & 7u;
+        b.r = __int_as_float(__float_as_int(b.r) + 8 * (int)(p.larger >> i & 1u) - 8 * (int)(p.smaller >> i & 1u));
+        b.mode = p.t_mid ? (int)(p.quotient >> i & 1u) : 2;
+    } else {
+        b.mode = HAS_T && !p.t_mid ? 2 : 1;
+    }
+    // the rounded quotient of a block that its scale saturates might overflow
+    if (b.mode == 1 && amax > 16.0f * b.d) b.mode = 2;
+    if (b.d == 0.0f) b.mode = 3;
+    if (!finite || (HAS_T && !p.t_ok)) {
+        b.byte = 0x7Fu;
+        b.mode = 3;
+    }
+    return b;
+}
+
+// Sixteen values of a block -> sixteen codes.
+template <typename T, bool NV, bool HAS_T>
+__device__ __forceinline__ void fp4_codes(const float (&x)[16], const Fp4Scale& b, uint32_t (&codes)[2]) {
+    constexpr bool MUL = !NV || (HAS_T && GridBits<T>::value > 0);   // mode 0 is the usual one
+    if (MUL) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float a = fabsf(x[8 * h + i]);
-                const float q0 = __fmul_rn(a, r);
-                const float e = __fmaf_rn(-q0, d, a);
-                float q = __fmaf_rn(e, r, q0);
-                if (HAS_T) q = odd_from_rn(q, a, d);
-                v[i] = copysignf(q, x[8 * h + i]);
+            for (int i = 0; i < 8; i += 2) {
+                const float2 q = f2_unpack(mul2s_rn(f2_pack(x[8 * h + i], x[8 * h + i + 1]), b.r));
+                v[i] = q.x;
+                v[i + 1] = q.y;
             }
             codes[h] = fp4_pack8(v);
         }
-    } else {
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i) {
-            float v = x[0];   // x[i] without a local-memory array
-#pragma unroll
-            for (int j = 1; j < 16; ++j) v = i == j ? x[j] : v;
-            const uint32_t n = fp4_code_exact(v, d) << (4 * (i & 7));
-            if (i < 8) codes[0] |= n;
-            else codes[1] |= n;
-        }
+        if (b.mode == 0) return;
     }
-    return byte;
+    if (b.mode == 3) {
+        codes[0] = codes[1] = 0u;
+        return;
+    }
+    if (!NV) return;
+    if (b.mode == 1) {
+        const unsigned long long r2 = f2_pack(b.r, b.r), nd2 = f2_pack(-b.d, -b.d);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float x0 = x[8 * h + i], x1 = x[8 * h + i + 1];
+                const unsigned long long a = HAS_T ? f2_pack(fabsf(x0), fabsf(x1)) : f2_pack(x0, x1);
+                const unsigned long long q0 = mul2s_rn(a, b.r);
+                const float2 q = f2_unpack(fma2_rn(fma2_rn(q0, nd2, a), r2, q0));
+                v[i] = HAS_T ? copysignf(odd_from_rn(q.x, fabsf(x0), b.d), x0) : q.x;
+                v[i + 1] = HAS_T ? copysignf(odd_from_rn(q.y, fabsf(x1), b.d), x1) : q.y;
+            }
+            codes[h] = fp4_pack8(v);
+        }
+        return;
+    }
+    codes[0] = codes[1] = 0u;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+        float v = x[0];   // x[i] without a local-memory array
+#pragma unroll
+        for (int j = 1; j < 16; ++j) v = i == j ? x[j] : v;
+        const uint32_t n = fp4_code_exact(v, b.d) << (4 * (i & 7));
+        if (i < 8) codes[0] |= n;
+        else codes[1] |= n;
+    }
 }
 
 // Bits of the largest |x| of sixteen, as an fp32 number's; NaN gives bits above infinity's.

@@ -85,6 +85,22 @@ template <typename T> struct Raw16 {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T); ++i) u[i] = make_uint4(0, 0, 0, 0);
     }
+    // bits of the largest |x| as an fp32 number's; NaN gives bits above infinity's
+    __device__ __forceinline__ uint32_t absmax() const {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+        if (sizeof(T) == 4) {
+            uint32_t m = 0u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+            return m;
+        }
+        uint32_t m = 0u;   // two 16-bit maxima: magnitudes order as integers
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7FFF7FFFu));
+        const uint16_t h = (uint16_t)max(m & 0xFFFFu, m >> 16);
+        return __float_as_uint(Elem<T>::to_f(*reinterpret_cast<const T*>(&h))) & 0x7FFFFFFFu;
+    }
     __device__ __forceinline__ void values(float (&v)[16]) const {
         const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
 #pragma unroll
@@ -99,17 +115,12 @@ template <typename T> struct Raw16 {
     }
 };
 
-// Quantize the sixteen values x of (row r of the tile, channel group g of the tile) into `codes`
-// and the scale byte of its block in the shared scale tiles.  Both lanes of an MX block call it.
-template <bool NV, bool HAS_T>
-__device__ __forceinline__ void quant_group(const float (&x)[16], const Fp4Tensor& t, int r, int g,
-                                            bool valid, uint8_t* sf, uint32_t (&codes)[2]) {
-    uint32_t amax = absmax16(x);
-    if (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    const uint32_t byte = fp4_quant16<NV, HAS_T>(x, amax, t, codes);
-    const int c = NV ? g : g >> 1;     // block of the tile's row
-    if (valid && (NV || !(g & 1)))
-        sf[(c >> 2) * kFp4TileBytes + fp4_tile_byte(r, c & 3)] = (uint8_t)byte;
+// The scale byte of the block of channel group g in row r of the CTA's tile, into its place in the
+// shared scale tiles (an MX block's from its first half's lane).
+template <bool NV>
+__device__ __forceinline__ void put_scale(uint8_t* sf, int r, int g, uint32_t byte) {
+    const int c = NV ? g : g >> 1;
+    if (NV || !(g & 1)) sf[(c >> 2) * kFp4TileBytes + fp4_tile_byte(r, c & 3)] = (uint8_t)byte;
 }
 
 __device__ __forceinline__ void store_codes(uint8_t* dst, const uint32_t (&c)[2], bool vec) {
@@ -122,7 +133,7 @@ __device__ __forceinline__ void store_codes(uint8_t* dst, const uint32_t (&c)[2]
 }
 
 template <typename T, bool NV, bool HAS_T, int LAYOUT>
-__global__ void __launch_bounds__(fp4q::THREADS)
+__global__ void __launch_bounds__(fp4q::THREADS, 4)
     fp4_quant_kernel(Fp4QuantParams p) {
     using namespace fp4q;
     constexpr int TILES = COLS / 4 / fp4_block(NV);   // scale tiles across the CTA's columns
@@ -141,7 +152,7 @@ __global__ void __launch_bounds__(fp4q::THREADS)
     rows_of_block(p.offsets, p.n_experts, p.M, rb, row0, n);
     if (n == 0) return;
     __syncthreads();   // the cleared scale tiles
-    const Fp4Tensor t = fp4_tensor(HAS_T ? p.tensor_scale : nullptr);
+    const Fp4Tensor t = fp4_tensor<T>(HAS_T ? p.tensor_scale : nullptr);
     const T* x = static_cast<const T*>(p.x);
 
     if (LAYOUT == COL) {
@@ -180,9 +191,9 @@ __global__ void __launch_bounds__(fp4q::THREADS)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = Elem<T>::to_f(buf[(g * 16 + j) * ROWS + r]);
                         uint32_t c[2];
-                        const uint32_t byte = fp4_quant16<NV, HAS_T>(v, absmax16(v), t, c);
-                        const int b = c0 / 16 + g;
-                        sf[(b >> 2) * kFp4TileBytes + fp4_tile_byte(r, b & 3)] = (uint8_t)byte;
+                        const Fp4Scale b = fp4_scale<T, NV, HAS_T>(absmax16(v), t);
+                        fp4_codes<T, NV, HAS_T>(v, b, c);
+                        put_scale<NV>(sf, r, c0 / 16 + g, b.byte);
                         store_codes(cbuf + r * CP + (c0 + g * 16) / 2, c, true);
                     }
                 }
@@ -194,15 +205,14 @@ __global__ void __launch_bounds__(fp4q::THREADS)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             v[j >> 4][j & 15] = Elem<T>::to_f(buf[(g * 32 + j) * ROWS + r]);
-                        const uint32_t amax = max(absmax16(v[0]), absmax16(v[1]));
-                        uint32_t c[2], byte = 0;
+                        const Fp4Scale b = fp4_scale<T, NV, HAS_T>(max(absmax16(v[0]), absmax16(v[1])), t);
+                        put_scale<NV>(sf, r, c0 / 16 + 2 * g, b.byte);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            byte = fp4_quant16<NV, HAS_T>(v[h], amax, t, c);
+                            uint32_t c[2];
+                            fp4_codes<T, NV, HAS_T>(v[h], b, c);
                             store_codes(cbuf + r * CP + (c0 + g * 32 + 16 * h) / 2, c, true);
                         }
-                        const int b = c0 / 32 + g;
-                        sf[(b >> 2) * kFp4TileBytes + fp4_tile_byte(r, b & 3)] = (uint8_t)byte;
                     }
                 }
             }
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(fp4q::THREADS)
         const int64_t k = k0 + g * 16;
         const bool k_ok = k < p.K;
         // K is a multiple of the block: a group of sixteen is whole, and so is an MX pair
-        constexpr int AHEAD = sizeof(T) == 4 ? 2 : 4;   // rows whose loads are in flight
+        constexpr int AHEAD = NV ? 2 : 4;   // rows whose loads are in flight, within 64 registers
         if (LAYOUT == VEC) {
 #pragma unroll 1
             for (int it = 0; it < PASSES; it += AHEAD) {
@@ -235,15 +245,25 @@ __global__ void __launch_bounds__(fp4q::THREADS)
                     if (k_ok && r < n) raw[a].load(x + (row0 + r) * p.sm + k);
                     else raw[a].zero();
                 }
+                // the blocks' scales first, side by side: each is a chain of dependent operations
+                Fp4Scale b[AHEAD];
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a) {
+                    uint32_t amax = raw[a].absmax();
+                    if (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                    b[a] = fp4_scale<T, NV, HAS_T>(amax, t);
+                }
 #pragma unroll
                 for (int a = 0; a < AHEAD; ++a) {
                     const int r = (it + a) * STEP + r0;
                     float v[16];
                     raw[a].values(v);
                     uint32_t c[2];
-                    quant_group<NV, HAS_T>(v, t, r, g, k_ok && r < n, sf, c);
-                    if (k_ok && r < n)
+                    fp4_codes<T, NV, HAS_T>(v, b[a], c);
+                    if (k_ok && r < n) {
+                        put_scale<NV>(sf, r, g, b[a].byte);
                         store_codes(p.codes + (row0 + r) * p.ldq + k / 2, c, p.codes_vec);
+                    }
                 }
             }
         } else {
@@ -255,10 +275,15 @@ __global__ void __launch_bounds__(fp4q::THREADS)
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     v[j] = k_ok && r < n ? Elem<T>::to_f(x[(row0 + r) * p.sm + (k + j) * p.sk]) : 0.0f;
+                uint32_t amax = absmax16(v);
+                if (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                const Fp4Scale b = fp4_scale<T, NV, HAS_T>(amax, t);
                 uint32_t c[2];
-                quant_group<NV, HAS_T>(v, t, r, g, k_ok && r < n, sf, c);
-                if (k_ok && r < n)
+                fp4_codes<T, NV, HAS_T>(v, b, c);
+                if (k_ok && r < n) {
+                    put_scale<NV>(sf, r, g, b.byte);
                     store_codes(p.codes + (row0 + r) * p.ldq + k / 2, c, p.codes_vec);
+                }
             }
         }
     }

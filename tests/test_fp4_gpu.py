@@ -112,7 +112,8 @@ def test_quant_layouts(fmt, dt, layout, M, K):
 
 
 @DT
-@pytest.mark.parametrize("t", [None, 1.0, 0.3, 1.7e-3, 3.0])
+@pytest.mark.parametrize("t", [None, 1.0, 0.3, 1.7e-3, 3.0] + [n / 2688 for n in (
+    79, 84, 63, 128, 101.5, 147, 201, 0.33, 6.5625, 255, 171)])
 def test_nv_borders(dt, t):
     """Values on and next to every border between two codes, for every E4M3 scale: x / (s t) on the
     border itself (rounded to x's type), one step below and one above."""

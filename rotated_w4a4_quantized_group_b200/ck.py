@@ -8,6 +8,7 @@ no CPU path.  Loading fails loudly if libck.so has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -399,13 +400,43 @@ def ck_unpack_w4(packed: torch.Tensor, K: int, out: torch.Tensor | None = None,
 
 
 # ------------------------------------------------------------------ microscaled fp4
+#
+# A small call's time is mostly the host's, so these functions check each tensor once and with the
+# cheapest accessors (get_device() is -1 for a host tensor), and enter a device context only when
+# another device is current.
 
+@functools.lru_cache(maxsize=4096)
 def fp4_scales_bytes(M: int, K: int, fmt: int, n_experts: int = 0) -> int:
     return int(lib().ck_fp4_scales_bytes(M, K, fmt, n_experts))
 
 
+@functools.lru_cache(maxsize=4096)
 def fp4_workspace_bytes(M: int, K: int, fmt: int, n_experts: int = 0) -> int:
     return int(lib().ck_fp4_linear_workspace_bytes(M, K, fmt, n_experts))
+
+
+_FLOAT_CODE = {torch.float32: CK_F32, torch.float16: CK_F16, torch.bfloat16: CK_BF16}
+
+
+def _on_device(x: torch.Tensor, *ts) -> int:
+    """x's CUDA device index; every other tensor must be there too."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"ck: tensor arguments must live on a CUDA device, got one on {x.device}")
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on {x.device}; got one on {t.device}")
+    return dev
+
+
+def _launch(fn, dev: int, stream, args):
+    """fn(*args, stream) with `dev` current, on the caller's stream or torch's current one."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return fn(*args, _stream(stream))
+    if stream is None:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    return fn(*args, _stream(stream))
 
 
 def _check_fp4(fmt: int, K: int):
@@ -416,7 +447,7 @@ def _check_fp4(fmt: int, K: int):
 
 
 def _check_codes(t: torch.Tensor, what: str, shape: tuple):
-    if t.dtype != torch.uint8 or tuple(t.shape) != shape or t.stride(-1) != 1:
+    if t.dtype != torch.uint8 or t.shape != shape or (t.stride(-1) != 1 and shape[-1] != 1):
         raise ValueError(f"{what} must be a uint8 {shape} view with unit inner stride; got "
                          f"{tuple(t.shape)} {t.dtype} strides {t.stride()}")
 
@@ -427,9 +458,7 @@ def _check_scales(t: torch.Tensor, what: str, nbytes: int):
                          f"{t.numel()} of {t.dtype}")
 
 
-def _check_tensor_scale(t: torch.Tensor | None, what: str, n: int, fmt: int):
-    if t is None:
-        return
+def _check_tensor_scale(t: torch.Tensor, what: str, n: int, fmt: int):
     if fmt == CK_MXFP4:
         raise ValueError(f"{what}: CK_MXFP4 has no tensor scale")
     if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
@@ -437,10 +466,8 @@ def _check_tensor_scale(t: torch.Tensor | None, what: str, n: int, fmt: int):
                          f"{t.dtype}")
 
 
-def _check_offsets(offsets: torch.Tensor | None) -> int:
-    """Number of experts (0 without offsets)."""
-    if offsets is None:
-        return 0
+def _check_offsets(offsets: torch.Tensor) -> int:
+    """Number of experts."""
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or \
             offsets.numel() < 2:
         raise ValueError("offsets must be a contiguous 1-D int32 tensor of one more value than "
@@ -449,9 +476,10 @@ def _check_offsets(offsets: torch.Tensor | None) -> int:
 
 
 def _float_code(t: torch.Tensor, what: str) -> int:
-    if t.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+    code = _FLOAT_CODE.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what} must be fp32, fp16 or bf16; got {t.dtype}")
-    return DTYPE_CODE[t.dtype]
+    return code
 
 
 def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None = None,
@@ -463,21 +491,27 @@ def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None
     M, K = x.shape
     _check_fp4(fmt, K)
     dt = _float_code(x, "x")
-    _same_device(x, tensor_scale, offsets, codes, scales)
-    _check_tensor_scale(tensor_scale, "tensor_scale", 1, fmt)
-    E = _check_offsets(offsets)
+    dev = _on_device(x, tensor_scale, offsets, codes, scales)
+    if tensor_scale is not None:
+        _check_tensor_scale(tensor_scale, "tensor_scale", 1, fmt)
+    E = 0 if offsets is None else _check_offsets(offsets)
     nbytes = fp4_scales_bytes(M, K, fmt, E)
+    half = K // 2
     if codes is None:
-        codes = torch.empty(M, (K // 2 + 15) // 16 * 16, dtype=torch.uint8,
-                            device=x.device)[:, : K // 2]
+        codes = torch.empty(M, (half + 15) // 16 * 16, dtype=torch.uint8, device=x.device)
+        if half % 16:
+            codes = codes[:, :half]
+    else:
+        _check_codes(codes, "codes", (M, half))
     if scales is None:
         scales = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    _check_codes(codes, "codes", (M, K // 2))
-    _check_scales(scales, "scales", nbytes)
-    with torch.cuda.device(x.device):
-        st = lib().ck_quant_fp4(_ptr(x), dt, M, K, x.stride(0), x.stride(1), fmt, _ptr(tensor_scale),
-                                _ptr(offsets), E, _ptr(codes), max(codes.stride(0), K // 2),
-                                _ptr(scales), _stream(stream))
+    else:
+        _check_scales(scales, "scales", nbytes)
+    sm, sk = x.stride()
+    st = _launch(lib().ck_quant_fp4, dev, stream, (
+        x.data_ptr(), dt, M, K, sm, sk, fmt, None if tensor_scale is None else tensor_scale.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), E, codes.data_ptr(),
+        max(codes.stride(0), half), scales.data_ptr()))
     _check(st, "ck_quant_fp4")
     return codes, scales
 
@@ -487,83 +521,98 @@ def ck_dequant_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: int, *,
                    out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
                    stream=None) -> torch.Tensor:
     """The values that codes (M, K/2) and their scale tiles stand for, (M, K)."""
-    M, K = codes.shape[0], 2 * codes.shape[1]
+    M, half = codes.shape
+    K = 2 * half
     _check_fp4(fmt, K)
-    _check_codes(codes, "codes", (M, K // 2))
-    _same_device(codes, scales, tensor_scale, offsets)
-    _check_tensor_scale(tensor_scale, "tensor_scale", 1, fmt)
-    E = _check_offsets(offsets)
+    dev = _on_device(codes, scales, tensor_scale, offsets)
+    _check_codes(codes, "codes", (M, half))
+    if tensor_scale is not None:
+        _check_tensor_scale(tensor_scale, "tensor_scale", 1, fmt)
+    E = 0 if offsets is None else _check_offsets(offsets)
     _check_scales(scales, "scales", fp4_scales_bytes(M, K, fmt, E))
     if out is None:
         out = torch.empty(M, K, dtype=out_dtype, device=codes.device)
-    _check_out(out, M, K, codes)
+    else:
+        _check_out(out, M, K, codes)
     odt = _float_code(out, "out")
-    with torch.cuda.device(codes.device):
-        st = lib().ck_dequant_fp4(_ptr(codes), max(codes.stride(0), K // 2), _ptr(scales), M, K, fmt,
-                                  _ptr(tensor_scale), _ptr(offsets), E, _ptr(out), odt,
-                                  max(out.stride(0), K), _stream(stream))
+    st = _launch(lib().ck_dequant_fp4, dev, stream, (
+        codes.data_ptr(), max(codes.stride(0), half), scales.data_ptr(), M, K, fmt,
+        None if tensor_scale is None else tensor_scale.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), E, out.data_ptr(), odt, max(out.stride(0), K)))
     _check(st, "ck_dequant_fp4")
     return out
 
 
-def _fp4_product(where: str, x, offsets, w, w_scales, fmt, bias, x_scales, x_tensor_scale,
-                 w_tensor_scale, out, out_dtype, workspace, dev_status, stream):
-    if x.dim() != 2 or w.dim() != 3:
-        raise ValueError("x must be 2-D and the weights (N, K/2), or (n_experts, N, K/2)")
-    E, N = w.shape[0], w.shape[1]
-    codes_in = x.dtype == torch.uint8
-    M, K = x.shape[0], x.shape[1] * 2 if codes_in else x.shape[1]
+def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_scale, w_tensor_scale,
+                 out, out_dtype, workspace, dev_status, stream):
+    """Both products: E weight matrices w of N channels; offsets None for the plain linear."""
+    M, K = x.shape
+    dt = _FLOAT_CODE.get(x.dtype)
+    if dt is None:
+        if x.dtype != torch.uint8:
+            raise ValueError(f"x must be fp32, fp16 or bf16, or uint8 codes; got {x.dtype}")
+        dt, K = CK_FP4, 2 * K
     _check_fp4(fmt, K)
-    _same_device(x, offsets, w, w_scales, bias, x_scales, x_tensor_scale, w_tensor_scale, workspace,
-                 dev_status)
-    _check_codes(w, "w_codes", (E, N, K // 2))
+    dev = _on_device(x, w, w_scales, bias, x_tensor_scale, w_tensor_scale, offsets, out, x_scales,
+                     workspace, dev_status)
+    half = K // 2
+    nE = 0 if offsets is None else E
+    if w.shape[-1] != half or w.dtype != torch.uint8 or w.stride(-1) != 1:
+        raise ValueError(f"w_codes must be uint8 of {half} bytes a row with unit inner stride; got "
+                         f"{tuple(w.shape)} {w.dtype} strides {w.stride()}")
     per = fp4_scales_bytes(N, K, fmt)
     _check_scales(w_scales, "w_scales", E * per)
-    if offsets is not None and (w_scales.dim() != 2 or tuple(w_scales.shape) != (E, per)):
-        raise ValueError(f"w_scales must be (n_experts, {per}); got {tuple(w_scales.shape)}")
-    _check_tensor_scale(x_tensor_scale, "x_tensor_scale", 1, fmt)
-    _check_tensor_scale(w_tensor_scale, "w_tensor_scale", E, fmt)
-    if offsets is not None and _check_offsets(offsets) != E:
-        raise ValueError(f"offsets must hold {E + 1} values for {E} experts; got {offsets.numel()}")
+    if nE:
+        if w_scales.shape != (E, per):
+            raise ValueError(f"w_scales must be (n_experts, {per}); got {tuple(w_scales.shape)}")
+        if _check_offsets(offsets) != E:
+            raise ValueError(f"offsets must hold {E + 1} values for {E} experts; got {offsets.numel()}")
+    if x_tensor_scale is not None:
+        _check_tensor_scale(x_tensor_scale, "x_tensor_scale", 1, fmt)
+    if w_tensor_scale is not None:
+        _check_tensor_scale(w_tensor_scale, "w_tensor_scale", E, fmt)
     bdt = CK_F32
     if bias is not None:
         bdt = _float_code(bias, "bias")
         if bias.numel() != E * N or not bias.is_contiguous():
             raise ValueError(f"bias must hold {E} x {N} contiguous values; got {tuple(bias.shape)}")
-    nE = 0 if offsets is None else E
-    if codes_in:
-        _check_codes(x, "x", (M, K // 2))
+    sm, sk = x.stride()
+    wsb, ws = 0, None
+    if dt == CK_FP4:
+        _check_codes(x, "x", (M, half))
         if x_scales is None:
             raise ValueError("x holds fp4 codes: x_scales must be given")
         _check_scales(x_scales, "x_scales", fp4_scales_bytes(M, K, fmt, nE))
-        dt = CK_FP4
+        sm, sk = max(sm, half), 1
     else:
-        dt = _float_code(x, "x")
-    if out is None:
-        if codes_in and out_dtype is None:
-            out_dtype = bias.dtype if bias is not None else torch.bfloat16
-        out = torch.empty(M, N, dtype=out_dtype or x.dtype, device=x.device)
-    _check_out(out, M, N, x)
-    odt = _float_code(out, "out")
-    with torch.cuda.device(x.device):
-        if workspace is None and not codes_in:
-            workspace = torch.empty(max(fp4_workspace_bytes(M, K, fmt, nE), 1), dtype=torch.uint8,
-                                    device=x.device)
-        wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        sm = max(x.stride(0), K // 2) if codes_in else x.stride(0)
-        ldo = max(out.stride(0), N)
-        if offsets is None:
-            st = lib().ck_fp4_linear(
-                _ptr(x), dt, M, K, sm, x.stride(1), fmt, _ptr(x_scales), _ptr(x_tensor_scale), _ptr(w),
-                N, w.stride(1), _ptr(w_scales), _ptr(w_tensor_scale), _ptr(bias), bdt, _ptr(out), odt,
-                ldo, _ptr(workspace), wsb, _ptr(dev_status), _stream(stream))
+        x_scales = None
+        if workspace is None:
+            wsb = fp4_workspace_bytes(M, K, fmt, nE)
+            if wsb:
+                workspace = torch.empty(wsb, dtype=torch.uint8, device=x.device)
+                ws = workspace.data_ptr()
         else:
-            st = lib().ck_fp4_expert_linear(
-                _ptr(x), dt, M, K, sm, x.stride(1), fmt, _ptr(x_scales), _ptr(x_tensor_scale),
-                _ptr(offsets), E, _ptr(w), N, w.stride(1), w.stride(0), _ptr(w_scales),
-                _ptr(w_tensor_scale), _ptr(bias), bdt, _ptr(out), odt, ldo, _ptr(workspace), wsb,
-                _ptr(dev_status), _stream(stream))
-    _check(st, where)
+            wsb = workspace.numel() * workspace.element_size()
+            ws = workspace.data_ptr()
+    if out is None:
+        if out_dtype is None:
+            out_dtype = x.dtype if dt != CK_FP4 else torch.bfloat16 if bias is None else bias.dtype
+        out = torch.empty(M, N, dtype=out_dtype, device=x.device)
+    else:
+        _check_out(out, M, N, x)
+    odt = _float_code(out, "out")
+    head = (x.data_ptr(), dt, M, K, sm, sk, fmt, None if x_scales is None else x_scales.data_ptr(),
+            None if x_tensor_scale is None else x_tensor_scale.data_ptr())
+    tail = (w_scales.data_ptr(), None if w_tensor_scale is None else w_tensor_scale.data_ptr(),
+            None if bias is None else bias.data_ptr(), bdt, out.data_ptr(), odt, max(out.stride(0), N),
+            ws, wsb, None if dev_status is None else dev_status.data_ptr())
+    w_ld = max(w.stride(-2), half)
+    if nE:
+        st = _launch(lib().ck_fp4_expert_linear, dev, stream, (
+            *head, offsets.data_ptr(), E, w.data_ptr(), N, w_ld, w.stride(0), *tail))
+    else:
+        st = _launch(lib().ck_fp4_linear, dev, stream, (*head, w.data_ptr(), N, w_ld, *tail))
+    _check(st, "ck_fp4_expert_linear" if nE else "ck_fp4_linear")
     return out
 
 
@@ -578,7 +627,7 @@ def ck_fp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor
     out (M, N)."""
     if w_codes.dim() != 2:
         raise ValueError(f"w_codes must be (N, K/2); got {tuple(w_codes.shape)}")
-    return _fp4_product("ck_fp4_linear", x, None, w_codes.unsqueeze(0), w_scales, fmt, bias, x_scales,
+    return _fp4_product(x, None, w_codes, 1, w_codes.shape[0], w_scales, fmt, bias, x_scales,
                         x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status, stream)
 
 
@@ -593,7 +642,9 @@ def ck_fp4_expert_linear(x: torch.Tensor, offsets: torch.Tensor, w_codes: torch.
     """ck_fp4_linear with rows sorted by expert: rows [offsets[e], offsets[e+1]) of x times
     w_codes[e] (n_experts, N, K/2) with w_scales[e] (n_experts, bytes), w_tensor_scale[e] and
     bias[e].  offsets stays on the device; rows of no expert keep what `out` held."""
-    if offsets is None:
-        raise ValueError("offsets must be given")
-    return _fp4_product("ck_fp4_expert_linear", x, offsets, w_codes, w_scales, fmt, bias, x_scales,
-                        x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status, stream)
+    if offsets is None or w_codes.dim() != 3:
+        raise ValueError("offsets must be given, and w_codes be (n_experts, N, K/2); got "
+                         f"{tuple(w_codes.shape)}")
+    return _fp4_product(x, offsets, w_codes, w_codes.shape[0], w_codes.shape[1], w_scales, fmt, bias,
+                        x_scales, x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status,
+                        stream)

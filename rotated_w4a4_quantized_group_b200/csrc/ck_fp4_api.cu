@@ -65,12 +65,14 @@ static ck_status product(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, 
     a.out_dt = out_dtype;
     a.ldo = ldo;
     a.dev_status = dev_status;
+    const bool few = !offsets && fp4_few_takes(M, K);
     if (codes_in) {
         a.codes = static_cast<const uint8_t*>(x);
         a.ldq = stride_m;
         a.scales = x_scales;
-        return launch_fp4_gemm(a, stream);
+        return few ? launch_fp4_few(a, nullptr, x_dtype, 0, 0, stream) : launch_fp4_gemm(a, stream);
     }
+    if (few && fp4_few_fuses(M, K)) return launch_fp4_few(a, x, x_dtype, stride_m, stride_k, stream);
     const size_t need = ck_fp4_linear_workspace_bytes(M, K, format, offsets ? n_experts : 0);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return CK_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -83,7 +85,7 @@ static ck_status product(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, 
     a.ldq = pitch;
     a.scales = scales;
     a.dependent = true;
-    return launch_fp4_gemm(a, stream);
+    return few ? launch_fp4_few(a, nullptr, x_dtype, 0, 0, stream) : launch_fp4_gemm(a, stream);
 }
 
 }  // namespace ck
@@ -99,6 +101,7 @@ size_t ck_fp4_scales_bytes(int64_t M, int64_t K, ck_fp4_format format, int n_exp
 
 size_t ck_fp4_linear_workspace_bytes(int64_t M, int64_t K, ck_fp4_format format, int n_experts) {
     if (!fp4_sizes(M, K, format) || n_experts < 0 || n_experts > kMaxExperts) return 0;
+    if (n_experts == 0 && fp4_few_fuses(M, K)) return 0;   // one launch, nothing to keep
     return (size_t)up(M * up(K / 2, 16), 256) + (size_t)scale_bytes(M, K, format, n_experts);
 }
 

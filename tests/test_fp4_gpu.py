@@ -338,7 +338,8 @@ def _close(got, exact, mag, K, what=""):
     assert worst <= 0, f"{what}: off by {worst:.3g} more than the bound"
 
 
-SHAPES = [(1, 1, 32), (1, 3840, 3840), (2, 40, 64), (5, 300, 96), (16, 130, 800), (31, 257, 1056),
+SHAPES = [(1, 1, 32), (1, 3840, 3840), (7, 200, 16384), (8, 96, 272), (9, 4000, 1040), (15, 333, 10240), (16, 129, 16400),
+          (17, 130, 12320), (40, 200, 12304), (2, 40, 64), (5, 300, 96), (16, 130, 800), (31, 257, 1056),
           (33, 640, 2080), (64, 128, 256), (65, 129, 288), (100, 1111, 2064), (127, 500, 512),
           (128, 256, 4096), (200, 384, 1024), (413, 1111, 2064), (700, 1920, 544), (1500, 2049, 1040),
           (2500, 3840, 320), (4097, 1300, 272)]

@@ -329,7 +329,10 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
                 }
             }
             loaded[rank][part] = issued;
-            if (rank != 0) dsmem_store_u32(&loaded[1][part], 0, issued);
+            if (rank != 0) {
+                dsmem_store_u32(&loaded[1][part], 0, issued);
+                fence_cluster();
+            }
         }
         __syncwarp();
     } else if (warp == WARP_MMA && rank == 0) {
@@ -411,6 +414,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
             if (CG == 2) {
                 dsmem_store_u32(&commits[0], 1, n_stage);
                 dsmem_store_u32(&commits[1], 1, n_acc);
+                fence_cluster();
             }
         }
         __syncwarp();
@@ -465,14 +469,19 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();   // rank 0's MMAs have completed, and the counts are there
-    if (tid == 0) {
-        if (rank == 0) {
-            // every copy has landed: what a producer did not issue of a stage that another did (after
-            // a timeout) its barrier is told not to expect
-            uint32_t n = 0;
-            for (int i = 0; i < 3 * CG; ++i) n = max(n, loaded[i / 3][i % 3]);
-            for (uint32_t j = n > S ? n - S : 0; j < n; ++j) {
+    // rank 0's MMAs have completed, and the counts are there (their writers' fences order them; a
+    // releasing barrier would wait for every output store to reach the L2)
+    if (CG == 2) cluster_sync_relaxed();
+    if (warp == 0) {
+        const uint32_t n = commits[0], a = commits[1];   // not larger than what was loaded
+        bool short_of = false;
+        for (int i = 0; i < 3 * CG; ++i) short_of |= loaded[i / 3][i % 3] != n;
+        if (short_of && rank == 0 && lane == 0) {
+            // after a timeout copies may still be in flight; what a producer did not issue of a stage
+            // that another did, the stage's barrier is told not to expect
+            uint32_t most = 0;
+            for (int i = 0; i < 3 * CG; ++i) most = max(most, loaded[i / 3][i % 3]);
+            for (uint32_t j = most > S ? most - S : 0; j < most; ++j) {
                 for (int part = 0; part < 3; ++part) {
                     const bool mine = j < loaded[0][part], other = CG == 2 ? j < loaded[1][part] : mine;
                     if (!mine && other) mbar_arrive_expect_tx(&full[j % S], part_bytes(part));
@@ -483,16 +492,15 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
             }
         }
         if (CG == 2) {
-            // the arrivals of rank 0's commits at this CTA's barriers have come
-            const uint32_t n = commits[0], a = commits[1];
-            for (uint32_t j = n > S ? n - S : 0; j < n; ++j)
-                mbar_wait(&empty[j % S], (j / S) & 1u, nullptr, p.dev_status);
-            for (uint32_t j = a > 2 ? a - 2 : 0; j < a; ++j)
-                mbar_wait(&acc_full[j & 1u], (j >> 1) & 1u, nullptr, p.dev_status);
+            // the arrivals of rank 0's commits at this CTA's barriers have come: a lane per barrier
+            const uint32_t slot = (uint32_t)lane;
+            if (slot < S && slot < n) mbar_wait(&empty[slot], ((n - 1 - slot) / S) & 1u, nullptr, p.dev_status);
+            if (slot < 2 && slot < a) mbar_wait(&acc_full[slot], ((a - 1 - slot) >> 1) & 1u, nullptr, p.dev_status);
+            __syncwarp();
         }
     }
     __syncthreads();
-    if (CG == 2) cluster_sync_all();
+    if (CG == 2) cluster_sync_relaxed();
     if (warp == WARP_MMA) {
         tc_fence_after();
         tmem_dealloc_cg<CG>(tmem_base, TMEM_COLS);

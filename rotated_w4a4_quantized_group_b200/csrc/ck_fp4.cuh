@@ -150,9 +150,9 @@ struct Fp4Tensor {
     float up;     // that power
     bool t_ok;    // a positive finite number; otherwise every scale is NaN
     bool t_mid;   // far enough from the ends for every s t and its reciprocal to be normal
-    // bit i: blocks whose scale has mantissa 1 + i / 8 want their reciprocal larger, smaller, or the
-    // rounded quotient
-    uint32_t larger, smaller, quotient;
+    // bits 4 i to 4 i + 3, signed: how many steps the reciprocal of blocks whose scale has mantissa
+    // 1 + i / 8 is moved; 1 where they take the rounded quotient instead
+    uint32_t moves;
 };
 
 // The tensor's constants; every lane of the warp calls it.
@@ -162,7 +162,7 @@ struct Fp4Tensor {
 // absmax / 2688, the usual calibration, every third block has such a border.  They want r a little
 // larger (x above its border), a little smaller (below), or exact; which depends on the mantissas of
 // s, border and t alone, so a warp finds it once for all 8 x 4 pairs.  In steps of a mantissa: r, the
-// product and the border are off by less than 3 together, so eight decide every such x, and no value
+// product and the border are off by less than 3 together, so seven decide every such x, and no value
 // further than 24 from its border is moved over it; the next value of the type is at least 2^12
 // steps away.
 template <typename T>
@@ -180,7 +180,7 @@ __device__ __forceinline__ Fp4Tensor fp4_tensor(const float* tensor_scale) {
         p.c = 1.0f;
     }
     p.rc = reciprocal(p.c);
-    p.larger = p.smaller = p.quotient = 0u;
+    p.moves = 0u;
     if (GRID > 0 && tensor_scale) {
         constexpr int mask = (1 << GRID) - 1;
         const int lane = threadIdx.x & 31;
@@ -193,25 +193,24 @@ __device__ __forceinline__ Fp4Tensor fp4_tensor(const float* tensor_scale) {
         const uint32_t up = __ballot_sync(0xffffffffu, near && e > 0.0f);
         const uint32_t down = __ballot_sync(0xffffffffu, near && e < 0.0f);
         const uint32_t on = __ballot_sync(0xffffffffu, near && e == 0.0f);
-        const int sh = 4 * (lane & 7);
+        const int sh = lane & 28;
         const bool u = (up >> sh & 15u) != 0u, w = (down >> sh & 15u) != 0u;
-        const bool bad = (on >> sh & 15u) != 0u || (u && w);
-        p.larger = __ballot_sync(0xffffffffu, lane < 8 && u && !bad);
-        p.smaller = __ballot_sync(0xffffffffu, lane < 8 && w && !bad);
-        p.quotient = __ballot_sync(0xffffffffu, lane < 8 && bad);
+        const int move = (on >> sh & 15u) != 0u || (u && w) ? 1 : u ? 7 : w ? -7 : 0;
+        p.moves = __reduce_or_sync(0xffffffffu, ((uint32_t)move & 15u) << sh);
     }
     return p;
 }
 
-// The E4M3 byte of amax / fl(6 t), rounded from the exact quotient: the quotient rounded correctly by
-// its residual, then to odd.  Where amax was scaled down into the subnormal range, or is there, the
-// quotient is below 2^-11 and rounds to zero whatever its last bits say; where it overflows, it
-// saturates.
+// The E4M3 byte of amax / fl(6 t), rounded from the exact quotient: the quotient rounded by its
+// residual, then to odd where it has so few bits that it may lie on a border.  Where amax was scaled
+// down into the subnormal range, or is there, the quotient is below 2^-11 and rounds to zero whatever
+// its last bits say; where it overflows (to a NaN, here), it saturates.
 __device__ __forceinline__ uint32_t nv_scale_byte(float amax, const Fp4Tensor& p) {
     const float a = __fmul_rn(amax, p.up);
     const float q0 = __fmul_rn(a, p.rc);
-    const float q = __fmaf_rn(__fmaf_rn(-q0, p.c, a), p.rc, q0);
-    return e4m3_byte(q0 < 1024.0f ? odd_from_rn(q, a, p.c) : 1024.0f);
+    float q = fminf(__fmaf_rn(__fmaf_rn(-q0, p.c, a), p.rc, q0), 1024.0f);
+    if ((__float_as_uint(q) & 0x7FFFFu) == 0u) q = odd_from_rn(q, a, p.c);
+    return e4m3_byte(q);
 }
 
 // One block's scale: its byte, the factor or divisor of its elements, and how they are divided.
@@ -230,18 +229,21 @@ struct Fp4Scale {
 //     rounded correctly (reciprocal, one residual, one correction: see RowDivisor): off a border it
 //     is at least 2^-24 of it away, so its rounding never moves it onto one.  d = fl(s t) has 24
 //     bits.  There 16-bit values take x * (1 / d), moved where a border falls next to one of them (see
-//     fp4_tensor), or else, as fp32 values do, the quotient rounded to odd.
+//     fp4_tensor), or else, as fp32 values do, the rounded quotient, and, where that is on a border,
+//     the quotient rounded to odd.
 template <typename T, bool NV, bool HAS_T>
 __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, const Fp4Tensor& p) {
     constexpr int GRID = GridBits<T>::value;
     Fp4Scale b;
-    const bool finite = amax_bits < 0x7F800000u;
     if (!NV) {
         b.byte = (uint32_t)max((int)(amax_bits >> 23) - 2, 0);
         b.r = __uint_as_float((254u - b.byte) << 23);   // 2^(127 - byte): exponent field 2 to 254
         b.d = 0.0f;
-        b.mode = finite ? 0 : 3;
-        if (!finite) b.byte = 0xFFu;
+        b.mode = 0;
+        if (amax_bits >= 0x7F800000u) {
+            b.byte = 0xFFu;
+            b.mode = 3;
+        }
         return b;
     }
     const float amax = __uint_as_float(amax_bits);
@@ -249,21 +251,28 @@ __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, const Fp4Tenso
     const float s = e4m3_value(b.byte);
     b.d = HAS_T ? __fmul_rn(s, p.t) : s;
     b.r = reciprocal(b.d);
+    b.mode = 1;
     if (HAS_T && GRID > 0) {
-        const uint32_t i = __float_as_uint(s) >> 20 & 7u;
-        b.r = __int_as_float(__float_as_int(b.r) + 8 * (int)(p.larger >> i & 1u) - 8 * (int)(p.smaller >> i & 1u));
-        b.mode = p.t_mid ? (int)(p.quotient >> i & 1u) : 2;
-    } else {
-        b.mode = HAS_T && !p.t_mid ? 2 : 1;
+        const uint32_t i4 = __float_as_uint(s) >> 18 & 28u;
+        const int move = (int)(p.moves << (i4 ^ 28u)) >> 28;
+        b.r = __int_as_float(__float_as_int(b.r) + move);
+        b.mode = move == 1 ? 1 : 0;
     }
     // the rounded quotient of a block that its scale saturates might overflow
-    if (b.mode == 1 && amax > 16.0f * b.d) b.mode = 2;
+    if (b.byte >= 0x7Eu && amax > 16.0f * b.d) b.mode = 2;
+    if (HAS_T && !p.t_mid) b.mode = 2;
     if (b.d == 0.0f) b.mode = 3;
-    if (!finite || (HAS_T && !p.t_ok)) {
+    if (amax_bits >= 0x7F800000u || (HAS_T && !p.t_ok)) {
         b.byte = 0x7Fu;
         b.mode = 3;
     }
     return b;
+}
+
+__device__ __forceinline__ float absmin3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
 }
 
 // Sixteen values of a block -> sixteen codes.
@@ -291,17 +300,38 @@ __device__ __forceinline__ void fp4_codes(const float (&x)[16], const Fp4Scale& 
     if (!NV) return;
     if (b.mode == 1) {
         const unsigned long long r2 = f2_pack(b.r, b.r), nd2 = f2_pack(-b.d, -b.d);
+        // A quotient on a border may have been rounded there.  All borders are multiples of 1/4:
+        // adding and taking away 1.5 * 2^21 rounds to those, and what changes nothing is one (or zero).
+        const unsigned long long big = f2_pack(0x1.8p21f, 0x1.8p21f);
+        float least = 1.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                const float x0 = x[8 * h + i], x1 = x[8 * h + i + 1];
-                const unsigned long long a = HAS_T ? f2_pack(fabsf(x0), fabsf(x1)) : f2_pack(x0, x1);
+                const unsigned long long a = f2_pack(x[8 * h + i], x[8 * h + i + 1]);
                 const unsigned long long q0 = mul2s_rn(a, b.r);
-                const float2 q = f2_unpack(fma2_rn(fma2_rn(q0, nd2, a), r2, q0));
-                v[i] = HAS_T ? copysignf(odd_from_rn(q.x, fabsf(x0), b.d), x0) : q.x;
-                v[i + 1] = HAS_T ? copysignf(odd_from_rn(q.y, fabsf(x1), b.d), x1) : q.y;
+                const unsigned long long q2 = fma2_rn(fma2_rn(q0, nd2, a), r2, q0);
+                const float2 q = f2_unpack(q2);
+                v[i] = q.x;
+                v[i + 1] = q.y;
+                if (HAS_T) {
+                    const float2 off = f2_unpack(sub2_rn(q2, sub2_rn(add2_rn(q2, big), big)));
+                    least = absmin3(least, off.x, off.y);
+                }
+            }
+            codes[h] = fp4_pack8(v);
+        }
+        const bool risky = least == 0.0f;
+        if (!HAS_T || !risky) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = fabsf(x[8 * h + i]), q0 = __fmul_rn(a, b.r);
+                const float q = __fmaf_rn(__fmaf_rn(-q0, b.d, a), b.r, q0);
+                v[i] = copysignf(odd_from_rn(q, a, b.d), x[8 * h + i]);
             }
             codes[h] = fp4_pack8(v);
         }
@@ -319,12 +349,19 @@ __device__ __forceinline__ void fp4_codes(const float (&x)[16], const Fp4Scale& 
     }
 }
 
+// max(|a|, |b|, |c|), NaN where one is NaN.
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
+}
+
 // Bits of the largest |x| of sixteen, as an fp32 number's; NaN gives bits above infinity's.
 __device__ __forceinline__ uint32_t absmax16(const float (&x)[16]) {
-    uint32_t m = 0u;
+    float m = absmax3(x[0], x[1], x[2]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    return m;
+    for (int i = 3; i < 15; i += 2) m = absmax3(m, x[i], x[i + 1]);
+    return __float_as_uint(absmax3(m, x[15], 0.0f));
 }
 
 }  // namespace ck

@@ -5,7 +5,7 @@
 //   dequantize: value = cvt(fl(fl(code * scale) * t))
 //
 // Both are one pass over memory, bound by HBM: K * sizeof(x) + K / 2 + K / block bytes a row.
-// A CTA takes 128 rows x 256 channels, so that it owns whole 512-byte scale tiles and writes each
+// A CTA takes 128 rows x 128 channels, so that it owns whole 512-byte scale tiles and writes each
 // of them as one contiguous run from shared memory; a thread takes sixteen channels of a row (an
 // NV block, or half an MX block whose other half is its neighbour lane's), with the loads of
 // several rows in flight.  Column-major input goes through a transposing shared-memory buffer.
@@ -22,7 +22,7 @@ namespace ck {
 namespace fp4q {
 constexpr int THREADS = 256;
 constexpr int ROWS = kFp4TileRows;    // rows of a CTA's tile
-constexpr int COLS = 256;             // channels of a CTA's tile
+constexpr int COLS = 128;             // channels of a CTA's tile
 constexpr int LANES = COLS / 16;      // threads across a row
 constexpr int STEP = THREADS / LANES; // rows a pass of the CTA covers
 constexpr int PASSES = ROWS / STEP;
@@ -84,22 +84,6 @@ template <typename T> struct Raw16 {
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T); ++i) u[i] = make_uint4(0, 0, 0, 0);
-    }
-    // bits of the largest |x| as an fp32 number's; NaN gives bits above infinity's
-    __device__ __forceinline__ uint32_t absmax() const {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
-        if (sizeof(T) == 4) {
-            uint32_t m = 0u;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
-            return m;
-        }
-        uint32_t m = 0u;   // two 16-bit maxima: magnitudes order as integers
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7FFF7FFFu));
-        const uint16_t h = (uint16_t)max(m & 0xFFFFu, m >> 16);
-        return __float_as_uint(Elem<T>::to_f(*reinterpret_cast<const T*>(&h))) & 0x7FFFFFFFu;
     }
     __device__ __forceinline__ void values(float (&v)[16]) const {
         const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
@@ -249,7 +233,9 @@ __global__ void __launch_bounds__(fp4q::THREADS, 4)
                 Fp4Scale b[AHEAD];
 #pragma unroll
                 for (int a = 0; a < AHEAD; ++a) {
-                    uint32_t amax = raw[a].absmax();
+                    float v[16];
+                    raw[a].values(v);
+                    uint32_t amax = absmax16(v);
                     if (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                     b[a] = fp4_scale<T, NV, HAS_T>(amax, t);
                 }

@@ -155,8 +155,6 @@ struct Fp4Tensor {
     uint32_t moves;
 };
 
-// The tensor's constants; every lane of the warp calls it.
-//
 // x * r, r within a step of 1 / d, d = fl(s t), rounds to the code of x / d for every x of a 16-bit
 // type but those on which a border (0.25 to 5; four mantissas) times d all but falls: with t an
 // absmax / 2688, the usual calibration, every third block has such a border.  They want r a little
@@ -164,10 +162,29 @@ struct Fp4Tensor {
 // s, border and t alone, so a warp finds it once for all 8 x 4 pairs.  In steps of a mantissa: r, the
 // product and the border are off by less than 3 together, so seven decide every such x, and no value
 // further than 24 from its border is moved over it; the next value of the type is at least 2^12
-// steps away.
+// steps away.  Every lane of the warp calls it; gives Fp4Tensor::moves.
 template <typename T>
-__device__ __forceinline__ Fp4Tensor fp4_tensor(const float* tensor_scale) {
+__device__ __forceinline__ uint32_t fp4_moves(float t) {
     constexpr int GRID = GridBits<T>::value;
+    constexpr int mask = (1 << GRID) - 1;
+    const int lane = threadIdx.x & 31;
+    const float tm = __uint_as_float((__float_as_uint(t) & 0x007FFFFFu) | 0x3F800000u);
+    const float d = __fmul_rn(1.0f + 0.125f * (lane >> 2), tm), m = 1.0f + 0.25f * (lane & 3);
+    const int b = __float_as_int(__fmul_rn(d, m));
+    const int g = (b + (mask + 1) / 2) & ~mask;              // the type's value nearest to d m
+    const float e = __fmaf_rn(-m, d, __int_as_float(g));     // its side, exactly
+    const bool near = abs(g - b) <= 24;
+    const uint32_t up = __ballot_sync(0xffffffffu, near && e > 0.0f);
+    const uint32_t down = __ballot_sync(0xffffffffu, near && e < 0.0f);
+    const uint32_t on = __ballot_sync(0xffffffffu, near && e == 0.0f);
+    const int sh = lane & 28;
+    const bool u = (up >> sh & 15u) != 0u, w = (down >> sh & 15u) != 0u;
+    const int move = (on >> sh & 15u) != 0u || (u && w) ? 1 : u ? 7 : w ? -7 : 0;
+    return __reduce_or_sync(0xffffffffu, ((uint32_t)move & 15u) << sh);
+}
+
+// The tensor's constants but for `moves`, which 16-bit values with a tensor scale need too.
+__device__ __forceinline__ Fp4Tensor fp4_tensor(const float* tensor_scale) {
     Fp4Tensor p;
     p.t = tensor_scale ? __ldg(tensor_scale) : 1.0f;
     p.t_ok = p.t > 0.0f && p.t <= 3.40282347e38f;
@@ -181,23 +198,6 @@ __device__ __forceinline__ Fp4Tensor fp4_tensor(const float* tensor_scale) {
     }
     p.rc = reciprocal(p.c);
     p.moves = 0u;
-    if (GRID > 0 && tensor_scale) {
-        constexpr int mask = (1 << GRID) - 1;
-        const int lane = threadIdx.x & 31;
-        const float tm = __uint_as_float((__float_as_uint(p.t) & 0x007FFFFFu) | 0x3F800000u);
-        const float d = __fmul_rn(1.0f + 0.125f * (lane >> 2), tm), m = 1.0f + 0.25f * (lane & 3);
-        const int b = __float_as_int(__fmul_rn(d, m));
-        const int g = (b + (mask + 1) / 2) & ~mask;              // the type's value nearest to d m
-        const float e = __fmaf_rn(-m, d, __int_as_float(g));     // its side, exactly
-        const bool near = abs(g - b) <= 24;
-        const uint32_t up = __ballot_sync(0xffffffffu, near && e > 0.0f);
-        const uint32_t down = __ballot_sync(0xffffffffu, near && e < 0.0f);
-        const uint32_t on = __ballot_sync(0xffffffffu, near && e == 0.0f);
-        const int sh = lane & 28;
-        const bool u = (up >> sh & 15u) != 0u, w = (down >> sh & 15u) != 0u;
-        const int move = (on >> sh & 15u) != 0u || (u && w) ? 1 : u ? 7 : w ? -7 : 0;
-        p.moves = __reduce_or_sync(0xffffffffu, ((uint32_t)move & 15u) << sh);
-    }
     return p;
 }
 
@@ -229,7 +229,7 @@ struct Fp4Scale {
 //     rounded correctly (reciprocal, one residual, one correction: see RowDivisor): off a border it
 //     is at least 2^-24 of it away, so its rounding never moves it onto one.  d = fl(s t) has 24
 //     bits.  There 16-bit values take x * (1 / d), moved where a border falls next to one of them (see
-//     fp4_tensor), or else, as fp32 values do, the rounded quotient, and, where that is on a border,
+//     fp4_moves), or else, as fp32 values do, the rounded quotient, and, where that is on a border,
 //     the quotient rounded to odd.
 template <typename T, bool NV, bool HAS_T>
 __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, const Fp4Tensor& p) {

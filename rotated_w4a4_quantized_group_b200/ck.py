@@ -403,7 +403,7 @@ def ck_unpack_w4(packed: torch.Tensor, K: int, out: torch.Tensor | None = None,
 #
 # A small call's time is mostly the host's, so these functions check each tensor once and with the
 # cheapest accessors (get_device() is -1 for a host tensor), and enter a device context only when
-# another device is current.
+# another device is current.  All of them also take stream=, as the functions above.
 
 @functools.lru_cache(maxsize=4096)
 def fp4_scales_bytes(M: int, K: int, fmt: int, n_experts: int = 0) -> int:
@@ -429,14 +429,28 @@ def _on_device(x: torch.Tensor, *ts) -> int:
     return dev
 
 
-def _launch(fn, dev: int, stream, args):
-    """fn(*args, stream) with `dev` current, on the caller's stream or torch's current one."""
+def _on_stream(fn):
+    """A caller's stream (a torch stream or a handle) becomes the current one for the whole call, so
+    that what the call allocates is allocated there too: memory freed on another stream may still be
+    in use by it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            t = next(a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor))
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _launch(fn, dev: int, args):
+    """fn(*args, stream) on torch's current stream of `dev`, with `dev` current."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return fn(*args, _stream(stream))
-    if stream is None:
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    return fn(*args, _stream(stream))
+            return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
 
 
 def _check_fp4(fmt: int, K: int):
@@ -482,9 +496,10 @@ def _float_code(t: torch.Tensor, what: str) -> int:
     return code
 
 
+@_on_stream
 def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None = None,
                  offsets: torch.Tensor | None = None, codes: torch.Tensor | None = None,
-                 scales: torch.Tensor | None = None, stream=None):
+                 scales: torch.Tensor | None = None):
     """A 2-D (M, K) view to microscaled fp4 (fmt CK_MXFP4 or CK_NVFP4); returns (codes uint8
     (M, K/2) with rows at a pitch of 16 bytes, scales uint8 in tiles).  offsets (n_experts + 1 int32
     on the device): rows sorted by expert, each expert's scales in tiles of its own."""
@@ -508,7 +523,7 @@ def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None
     else:
         _check_scales(scales, "scales", nbytes)
     sm, sk = x.stride()
-    st = _launch(lib().ck_quant_fp4, dev, stream, (
+    st = _launch(lib().ck_quant_fp4, dev, (
         x.data_ptr(), dt, M, K, sm, sk, fmt, None if tensor_scale is None else tensor_scale.data_ptr(),
         None if offsets is None else offsets.data_ptr(), E, codes.data_ptr(),
         max(codes.stride(0), half), scales.data_ptr()))
@@ -516,10 +531,10 @@ def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None
     return codes, scales
 
 
+@_on_stream
 def ck_dequant_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: int, *,
                    tensor_scale: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
-                   out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
-                   stream=None) -> torch.Tensor:
+                   out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values that codes (M, K/2) and their scale tiles stand for, (M, K)."""
     M, half = codes.shape
     K = 2 * half
@@ -535,7 +550,7 @@ def ck_dequant_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: int, *,
     else:
         _check_out(out, M, K, codes)
     odt = _float_code(out, "out")
-    st = _launch(lib().ck_dequant_fp4, dev, stream, (
+    st = _launch(lib().ck_dequant_fp4, dev, (
         codes.data_ptr(), max(codes.stride(0), half), scales.data_ptr(), M, K, fmt,
         None if tensor_scale is None else tensor_scale.data_ptr(),
         None if offsets is None else offsets.data_ptr(), E, out.data_ptr(), odt, max(out.stride(0), K)))
@@ -544,7 +559,7 @@ def ck_dequant_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: int, *,
 
 
 def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_scale, w_tensor_scale,
-                 out, out_dtype, workspace, dev_status, stream):
+                 out, out_dtype, workspace, dev_status):
     """Both products: E weight matrices w of N channels; offsets None for the plain linear."""
     M, K = x.shape
     dt = _FLOAT_CODE.get(x.dtype)
@@ -608,29 +623,31 @@ def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_sc
             ws, wsb, None if dev_status is None else dev_status.data_ptr())
     w_ld = max(w.stride(-2), half)
     if nE:
-        st = _launch(lib().ck_fp4_expert_linear, dev, stream, (
+        st = _launch(lib().ck_fp4_expert_linear, dev, (
             *head, offsets.data_ptr(), E, w.data_ptr(), N, w_ld, w.stride(0), *tail))
     else:
-        st = _launch(lib().ck_fp4_linear, dev, stream, (*head, w.data_ptr(), N, w_ld, *tail))
+        st = _launch(lib().ck_fp4_linear, dev, (*head, w.data_ptr(), N, w_ld, *tail))
     _check(st, "ck_fp4_expert_linear" if nE else "ck_fp4_linear")
     return out
 
 
+@_on_stream
 def ck_fp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, fmt: int,
                   bias: torch.Tensor | None = None, *, x_scales: torch.Tensor | None = None,
                   x_tensor_scale: torch.Tensor | None = None,
                   w_tensor_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
                   out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
-                  dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                  dev_status: torch.Tensor | None = None) -> torch.Tensor:
     """The linear on microscaled fp4: x (M, K) activations (quantized on the way), or uint8 codes
     (M, K/2) with x_scales; w_codes (N, K/2) and w_scales as ck_quant_fp4 returns them.  Returns
     out (M, N)."""
     if w_codes.dim() != 2:
         raise ValueError(f"w_codes must be (N, K/2); got {tuple(w_codes.shape)}")
     return _fp4_product(x, None, w_codes, 1, w_codes.shape[0], w_scales, fmt, bias, x_scales,
-                        x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status, stream)
+                        x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status)
 
 
+@_on_stream
 def ck_fp4_expert_linear(x: torch.Tensor, offsets: torch.Tensor, w_codes: torch.Tensor,
                          w_scales: torch.Tensor, fmt: int, bias: torch.Tensor | None = None, *,
                          x_scales: torch.Tensor | None = None,
@@ -638,7 +655,7 @@ def ck_fp4_expert_linear(x: torch.Tensor, offsets: torch.Tensor, w_codes: torch.
                          w_tensor_scale: torch.Tensor | None = None,
                          out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                          workspace: torch.Tensor | None = None,
-                         dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                         dev_status: torch.Tensor | None = None) -> torch.Tensor:
     """ck_fp4_linear with rows sorted by expert: rows [offsets[e], offsets[e+1]) of x times
     w_codes[e] (n_experts, N, K/2) with w_scales[e] (n_experts, bytes), w_tensor_scale[e] and
     bias[e].  offsets stays on the device; rows of no expert keep what `out` held."""
@@ -646,5 +663,4 @@ def ck_fp4_expert_linear(x: torch.Tensor, offsets: torch.Tensor, w_codes: torch.
         raise ValueError("offsets must be given, and w_codes be (n_experts, N, K/2); got "
                          f"{tuple(w_codes.shape)}")
     return _fp4_product(x, offsets, w_codes, w_codes.shape[0], w_codes.shape[1], w_scales, fmt, bias,
-                        x_scales, x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status,
-                        stream)
+                        x_scales, x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status)

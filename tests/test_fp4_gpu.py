@@ -338,7 +338,7 @@ def _close(got, exact, mag, K, what=""):
     assert worst <= 0, f"{what}: off by {worst:.3g} more than the bound"
 
 
-SHAPES = [(1, 1, 32), (1, 3840, 3840), (7, 200, 16384), (8, 96, 272), (9, 4000, 1040), (15, 333, 10240), (16, 129, 16400),
+SHAPES = [(1, 1, 32), (3, 5, 16), (70, 9, 16), (1, 3840, 3840), (7, 200, 16384), (8, 96, 272), (9, 4000, 1040), (15, 333, 10240), (16, 129, 16400),
           (17, 130, 12320), (40, 200, 12304), (2, 40, 64), (5, 300, 96), (16, 130, 800), (31, 257, 1056),
           (33, 640, 2080), (64, 128, 256), (65, 129, 288), (100, 1111, 2064), (127, 500, 512),
           (128, 256, 4096), (200, 384, 1024), (413, 1111, 2064), (700, 1920, 544), (1500, 2049, 1040),
@@ -441,3 +441,318 @@ def test_expert_linear(fmt, name, N, K):
             exact, mag = exact + bias[e].double(), mag + bias[e].double().abs()
         _close(out[lo:hi, :N], exact, mag, K, f"expert {e}")
     assert (out[rest] == -7.5).all() and (out[:, N:] == -7.5).all()
+
+
+# ------------------------------------------------------------------- values that are not numbers
+
+@FMT
+@pytest.mark.parametrize("M,N", [(6, 200), (40, 200), (300, 1000)])
+def test_nan_stays_in_its_row_and_channel(fmt, M, N):
+    """A NaN activation makes its row's outputs NaN, a weight block with a NaN scale its channel's,
+    and nothing else."""
+    K = 320
+    x = _x(M, K, BF16, 20, spread=False)
+    x[2, 70] = float("nan")
+    x[5, 300] = float("inf")
+    w, ws, wv = _weights(1, N, K, fmt, 21)
+    n = N - 60
+    ws[0, ref.tile_index([n], K // ref.BLOCK[fmt])[0, 3]] = 0xFF if fmt == MX else 0x7F
+    out = ck.ck_fp4_linear(x.cuda(), w[0], ws[0], fmt)
+    bad = torch.isnan(out).cpu()
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[2], want[5], want[:, n] = True, True, True
+    assert torch.equal(bad, want)
+    xv = _xvalues(x, fmt, None).nan_to_num(0.0)
+    exact, mag = xv @ wv[0].t(), xv.abs() @ wv[0].abs().t()
+    keep = ~want.cuda()
+    _close(out[keep], exact[keep], mag[keep], K)
+
+
+def test_fp16_output_overflows_to_infinity():
+    x = torch.full((40, 64), 6.0, dtype=F16)
+    w = torch.from_numpy(ref.pack(np.full((8, 64), 7, np.uint8))).cuda()
+    ws = torch.from_numpy(ref.tile(np.full((8, 2), 140, np.uint8))).cuda()      # 2^13
+    out = ck.ck_fp4_linear(x.cuda(), w, ws, MX)
+    assert torch.isinf(out).all() and (out > 0).all()
+
+
+# ------------------------------------------------------------------- how calls are made
+
+def _case(fmt, M, N, K, dt=BF16, seed=30):
+    x = _x(M, K, dt, seed, spread=False).cuda()
+    w, ws, _ = _weights(1, N, K, fmt, seed + 1)
+    return x, w[0], ws[0]
+
+
+@FMT
+@pytest.mark.parametrize("M", [3, 40, 500])
+def test_same_bits_every_time(fmt, M):
+    x, w, ws = _case(fmt, M, 700, 1056)
+    first = ck.ck_fp4_linear(x, w, ws, fmt)
+    for _ in range(5):
+        assert torch.equal(first, ck.ck_fp4_linear(x, w, ws, fmt))
+
+
+@FMT
+@pytest.mark.parametrize("M", [1, 17, 64, 65, 300])
+def test_codes_in_equal_activations_in(fmt, M):
+    """ck_quant_fp4 and then the product of codes gives the bits of the product of activations, also
+    where that quantizes inside its own kernel."""
+    x, w, ws = _case(fmt, M, 333, 1056)
+    t = _t(0.031) if fmt == NV else None
+    codes, scales = ck.ck_quant_fp4(x, fmt, tensor_scale=t)
+    a = ck.ck_fp4_linear(x, w, ws, fmt, x_tensor_scale=t)
+    b = ck.ck_fp4_linear(codes, w, ws, fmt, x_scales=scales, x_tensor_scale=t)
+    assert a.dtype == b.dtype == BF16 and torch.equal(a, b)
+
+
+@FMT
+@pytest.mark.parametrize("layout", ["pitch", "odd", "cols", "second"])
+@pytest.mark.parametrize("M", [5, 40])
+def test_linear_of_any_layout(fmt, layout, M):
+    x, w, ws = _case(fmt, M, 130, 544)
+    assert torch.equal(ck.ck_fp4_linear(x, w, ws, fmt),
+                       ck.ck_fp4_linear(_place(x.cpu(), layout), w, ws, fmt))
+
+
+@FMT
+@pytest.mark.parametrize("M", [9, 40, 200])
+def test_output_pitch_and_guards(fmt, M):
+    N = 130
+    x, w, ws = _case(fmt, M, N, 288)
+    ref_out = ck.ck_fp4_linear(x, w, ws, fmt)
+    for pad, first in ((6, 0), (8, 8), (7, 3)):
+        buf = torch.full((M + 2, N + pad + first), -7.5, dtype=BF16, device="cuda")
+        ck.ck_fp4_linear(x, w, ws, fmt, out=buf[1: M + 1, first: N + first])
+        assert torch.equal(buf[1: M + 1, first: N + first], ref_out)
+        buf[1: M + 1, first: N + first] = -7.5
+        assert (buf == -7.5).all()
+
+
+@FMT
+@pytest.mark.parametrize("M", [4, 50, 300])
+def test_captured_and_replayed_on_new_inputs(fmt, M):
+    """A captured call follows its buffers; two graphs captured one after the other do not disturb each
+    other."""
+    x, w, ws = _case(fmt, M, 400, 544)
+    y = x.clone()
+    ck.ck_fp4_linear(x, w, ws, fmt)
+    torch.cuda.synchronize()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        o1 = ck.ck_fp4_linear(x, w, ws, fmt)
+    with torch.cuda.graph(g2):
+        c2, s2 = ck.ck_quant_fp4(y, fmt)
+        o2 = ck.ck_fp4_linear(c2, w, ws, fmt, x_scales=s2)
+    for k in range(3):
+        x.copy_(_x(M, 544, BF16, 40 + k, spread=False))
+        y.copy_(_x(M, 544, BF16, 50 + k, spread=False))
+        g1.replay()
+        g2.replay()
+        g1.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o1, ck.ck_fp4_linear(x, w, ws, fmt))
+        assert torch.equal(o2, ck.ck_fp4_linear(y, w, ws, fmt))
+
+
+@FMT
+def test_captured_expert_call_follows_its_offsets(fmt):
+    M, N, K, E = 300, 260, 288, 5
+    x = _x(M, K, BF16, 60, spread=False).cuda()
+    w, ws, _ = _weights(E, N, K, fmt, 61)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    out = torch.empty(M, N, dtype=BF16, device="cuda")
+    ck.ck_fp4_expert_linear(x, off, w, ws, fmt, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ck.ck_fp4_expert_linear(x, off, w, ws, fmt, out=out)
+    for o in ([0, 100, 100, 200, 290, 300], [0, 0, 0, 0, 0, 300], [7, 8, 9, 10, 11, 12], [0] * 6):
+        off.copy_(torch.tensor(o, dtype=torch.int32))
+        out.fill_(-7.5)
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        for e in range(E):
+            if o[e + 1] > o[e]:
+                one = ck.ck_fp4_linear(x[o[e]:o[e + 1]], w[e], ws[e], fmt)
+                # the same codes and products; the sums' order may differ between the kernels
+                assert torch.allclose(got[o[e]:o[e + 1]].float(), one.float(), rtol=2 ** -7, atol=1e-3)
+        assert (got[:o[0]] == -7.5).all() and (got[o[-1]:] == -7.5).all()
+
+
+@FMT
+@pytest.mark.parametrize("M", [12, 48, 400])
+def test_two_calls_at_once_on_two_streams(fmt, M):
+    x, w, ws = _case(fmt, M, 1000, 2080)
+    y = _x(M, 2080, BF16, 70, spread=False).cuda()
+    want = ck.ck_fp4_linear(x, w, ws, fmt), ck.ck_fp4_linear(y, w, ws, fmt)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    for _ in range(6):
+        got[0].append(ck.ck_fp4_linear(x, w, ws, fmt, stream=s[0]))
+        got[1].append(ck.ck_fp4_linear(y, w, ws, fmt, stream=s[1].cuda_stream))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(o, b) for o in a)
+
+
+def test_callers_workspace_and_its_layout():
+    M, N, K = 100, 200, 544
+    x, w, ws = _case(NV, M, N, K)
+    need = ck.fp4_workspace_bytes(M, K, NV)
+    buf = torch.full((need + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = ck.ck_fp4_linear(x, w, ws, NV, workspace=buf)
+    assert torch.equal(out, ck.ck_fp4_linear(x, w, ws, NV)) and (buf[need:] == 0x5A).all()
+    codes, scales = ck.ck_quant_fp4(x, NV)
+    pitch = -(-K // 2 // 16) * 16
+    at = -(-M * pitch // 256) * 256
+    assert torch.equal(buf[: M * pitch].view(M, pitch)[:, : K // 2], codes)
+    assert torch.equal(buf[at: at + scales.numel()], scales)
+    with pytest.raises(ck.CkError):
+        ck.ck_fp4_linear(x, w, ws, NV, workspace=buf[: need - 256])
+
+
+def test_binding_refuses_what_does_not_fit():
+    x, w, ws = _case(NV, 20, 64, 128)
+    wt, off = _t(0.1), torch.tensor([0, 10, 20], dtype=torch.int32, device="cuda")
+    w2, ws2, _ = _weights(2, 64, 128, NV, 80)
+    bad = [lambda: ck.ck_fp4_linear(x, w[:, :60], ws, NV), lambda: ck.ck_fp4_linear(x, w, ws[:100], NV),
+           lambda: ck.ck_fp4_linear(x, w, ws, NV, torch.zeros(63, device="cuda")),
+           lambda: ck.ck_fp4_linear(x, w, ws, NV, out=torch.empty(20, 63, device="cuda")),
+           lambda: ck.ck_fp4_linear(x, w, ws, MX, x_tensor_scale=wt),
+           lambda: ck.ck_fp4_linear(x, w, ws, NV, w_tensor_scale=wt.double()),
+           lambda: ck.ck_fp4_linear(x, w, ws, NV, w_tensor_scale=torch.ones(2, device="cuda")),
+           lambda: ck.ck_fp4_linear(x.byte()[:, :64], w, ws, NV),
+           lambda: ck.ck_fp4_linear(x, w.cpu(), ws, NV), lambda: ck.ck_fp4_linear(x, w.t(), ws, NV),
+           lambda: ck.ck_fp4_expert_linear(x, off[:2], w2, ws2, NV),
+           lambda: ck.ck_fp4_expert_linear(x, off.long(), w2, ws2, NV),
+           lambda: ck.ck_fp4_expert_linear(x, off, w2, ws2[:, :-512], NV),
+           lambda: ck.ck_fp4_expert_linear(x, off, w2, ws2, NV, torch.zeros(64, device="cuda")),
+           lambda: ck.ck_quant_fp4(x, NV, tensor_scale=torch.ones(2, device="cuda")),
+           lambda: ck.ck_quant_fp4(x, NV, codes=torch.empty(20, 63, dtype=torch.uint8, device="cuda")),
+           lambda: ck.ck_quant_fp4(x, NV, scales=torch.empty(10, dtype=torch.uint8, device="cuda")),
+           lambda: ck.ck_dequant_fp4(w, ws[:64], NV), lambda: ck.ck_dequant_fp4(w.char(), ws, NV)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    # weights at a pitch that TMA cannot read are refused by the library
+    odd = torch.zeros(64, 72, dtype=torch.uint8, device="cuda")[:, :64]
+    with pytest.raises(ck.CkError):
+        ck.ck_fp4_linear(x, odd, ws, NV)
+
+
+def test_past_two_to_the_31():
+    """Rows whose element offsets need more than 32 bits: the last rows are right, in and out."""
+    M, K, N = 140000, 16384, 16400
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty(M, K, dtype=BF16, device="cuda").normal_(generator=g)
+    codes, scales = ck.ck_quant_fp4(x, NV)
+    y = ck.ck_dequant_fp4(codes, scales, NV)
+    last = x[-3:].cpu()
+    rc, rs = ref.quantize(last, NV)
+    np.testing.assert_array_equal(ref.unpack(codes[-3:].cpu().numpy()), rc)
+    np.testing.assert_array_equal(y[-3:].float().cpu().numpy().astype(np.float64), ref.values(rc, rs, NV))
+    del y, codes, scales
+    w, ws, wv = _weights(1, N, 64, NV, 6)
+    out = ck.ck_fp4_linear(x[:, :64], w[0], ws[0], NV)
+    xv = _xvalues(x[-3:, :64].cpu(), NV, None)
+    _close(out[-3:], xv @ wv[0].t(), xv.abs() @ wv[0].abs().t(), 64)
+
+
+# ------------------------------------------------------------------- together
+
+@FMT
+def test_a_mixture_of_experts_layer(fmt):
+    """Router, sort, up projection, activation, down projection, weighted sum back: the operators as a
+    layer uses them, its weights quantized by them too.  Each step is compared on the inputs that it
+    got, so that no rounding of one step hides in another's tolerance."""
+    T, D, H, E, top = 90, 320, 544, 6, 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    tok = torch.randn(T, D, device="cuda", generator=g, dtype=BF16)
+    up = torch.randn(E, H, D, device="cuda", generator=g) * 0.06
+    down = torch.randn(E, D, H, device="cuda", generator=g) * 0.06
+
+    def quantized(w):
+        t = w.abs().amax((1, 2)) / (6 * 448) if fmt == NV else None
+        both = [ck.ck_quant_fp4(w[e], fmt, tensor_scale=None if t is None else t[e: e + 1])
+                for e in range(E)]
+        # contiguous rows of 16-byte multiples, as the widths here are
+        return torch.stack([c for c, _ in both]), torch.stack([s for _, s in both]), t
+
+    def values(q):
+        c, s, t = (v if v is None else v.cpu().numpy() for v in q)
+        k = 2 * c.shape[-1] // ref.BLOCK[fmt]
+        v = np.stack([ref.values(ref.unpack(c[e]), ref.untile(s[e], c.shape[1], k), fmt) for e in range(E)])
+        return torch.from_numpy(v if t is None else v * t.astype(np.float64)[:, None, None]).cuda()
+
+    qu, qd = quantized(up), quantized(down)
+    prob, pick = torch.randn(T, E, device="cuda", generator=g).softmax(-1).topk(top)
+    order = pick.flatten().argsort(stable=True)
+    rows = order // top
+    count = torch.bincount(pick.flatten(), minlength=E)
+    off = torch.cat([count.new_zeros(1), count.cumsum(0)]).int()
+
+    def expert(x, q, out_dtype):
+        out = ck.ck_fp4_expert_linear(x, off, q[0], q[1], fmt, w_tensor_scale=q[2], out_dtype=out_dtype)
+        v, xv, o = values(q), _xvalues(x.cpu(), fmt, None), off.tolist()
+        for e in range(E):
+            a = xv[o[e]: o[e + 1]]
+            _close(out[o[e]: o[e + 1]], a @ v[e].t(), a.abs() @ v[e].abs().t(), x.shape[1], f"expert {e}")
+        return out
+
+    h = expert(tok[rows], qu, BF16)
+    h = torch.nn.functional.silu(h.float()).to(BF16)
+    z = expert(h, qd, F32)
+    y = torch.zeros(T, D, device="cuda").index_add_(0, rows, z * prob.flatten()[order][:, None])
+    # The whole layer against the unquantized one.  E2M1's half step is at most a quarter of the value,
+    # about 0.25 / sqrt(3) of it in the mean (0.14); four operands in two products, independent: 0.29.
+    full = torch.zeros(T, D, device="cuda", dtype=torch.float64)
+    for i in range(T):
+        for j in range(top):
+            e = int(pick[i, j])
+            a = torch.nn.functional.silu(tok[i].double() @ up[e].double().t())
+            full[i] += prob[i, j].double() * (a @ down[e].double().t())
+    assert (y.double() - full).norm() < 0.35 * full.norm()
+
+
+# ------------------------------------------------------------------- waits that run out
+
+@FMT
+@pytest.mark.parametrize("what,M,N,K,E", [("few rows, from activations", 8, 512, 1024, 0),
+                                          ("few rows, from codes", 40, 512, 1024, 0),
+                                          ("one CTA a tile", 200, 256, 1024, 0),
+                                          ("two CTAs a tile", 3000, 2048, 1024, 0),
+                                          ("by expert", 300, 512, 1024, 4)])
+def test_wait_expiry_returns_a_status(fmt, what, M, N, K, E):
+    """The build whose role waits give up at once: the call returns CK_OK, the status word says timeout,
+    and a normal call afterwards is right."""
+    L = ck.load_library(os.path.join(os.path.dirname(ck.LIB_PATH), "libck_test_waits.so"))
+    x = _x(M, K, BF16, 90, spread=False).cuda()
+    w, ws, wv = _weights(max(E, 1), N, K, fmt, 91)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.empty(M, N, dtype=BF16, device="cuda")
+    work = torch.empty(max(ck.fp4_workspace_bytes(M, K, fmt, E), 256), dtype=torch.uint8, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    head = (x.data_ptr(), ck.CK_BF16, M, K, K, 1, fmt, None, None)
+    tail = (ws.data_ptr(), None, None, 0, out.data_ptr(), ck.CK_BF16, N, work.data_ptr(), work.numel(),
+            status.data_ptr(), st)
+    if E:
+        off = torch.tensor([0, 100, 100, 250, 300], dtype=torch.int32, device="cuda")
+        rc = L.ck_fp4_expert_linear(*head, off.data_ptr(), E, w.data_ptr(), N, K // 2, w.stride(0), *tail)
+    else:
+        rc = L.ck_fp4_linear(*head, w.data_ptr(), N, K // 2, *tail)
+    assert rc == ck.CK_OK
+    torch.cuda.synchronize()
+    assert status.item() == ck.CK_ERR_TIMEOUT, what
+    status.zero_()
+    if not E:
+        good = ck.ck_fp4_linear(x, w[0], ws[0], fmt, dev_status=status)
+        xv = _xvalues(x.cpu(), fmt, None)
+        _close(good, xv @ wv[0].t(), xv.abs() @ wv[0].abs().t(), K, what)
+    else:
+        good = ck.ck_fp4_expert_linear(x, off, w, ws, fmt, dev_status=status)
+        xv = _xvalues(x[:100].cpu(), fmt, None)
+        _close(good[:100], xv @ wv[0].t(), xv.abs() @ wv[0].abs().t(), K, what)
+    assert status.item() == 0

@@ -403,7 +403,7 @@ def ck_unpack_w4(packed: torch.Tensor, K: int, out: torch.Tensor | None = None,
 #
 # A small call's time is mostly the host's, so these functions check each tensor once and with the
 # cheapest accessors (get_device() is -1 for a host tensor), and enter a device context only when
-# another device is current.  All of them also take stream=, as the functions above.
+# another device is current.
 
 @functools.lru_cache(maxsize=4096)
 def fp4_scales_bytes(M: int, K: int, fmt: int, n_experts: int = 0) -> int:
@@ -429,28 +429,25 @@ def _on_device(x: torch.Tensor, *ts) -> int:
     return dev
 
 
-def _on_stream(fn):
-    """A caller's stream (a torch stream or a handle) becomes the current one for the whole call, so
-    that what the call allocates is allocated there too: memory freed on another stream may still be
-    in use by it."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        if not isinstance(stream, torch.cuda.Stream):
-            t = next(a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor))
-            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
+def _on_stream(stream, like: torch.Tensor, fn, *args, **kw):
+    """fn(*args, **kw) with a caller's stream (a torch stream or a handle) current, so that what the
+    call allocates is allocated there too: memory freed on another stream may still be in use by it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
-def _launch(fn, dev: int, args):
-    """fn(*args, stream) on torch's current stream of `dev`, with `dev` current."""
-    if dev != torch.cuda.current_device():
+def _launch(name: str, dev: int, args):
+    """The library's `name` on torch's current stream of `dev`, with `dev` current."""
+    fn = getattr(_lib or lib(), name)
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
         with torch.cuda.device(dev):
-            return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != CK_OK:
+        raise CkError(st, name)
 
 
 def _check_fp4(fmt: int, K: int):
@@ -496,13 +493,15 @@ def _float_code(t: torch.Tensor, what: str) -> int:
     return code
 
 
-@_on_stream
 def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None = None,
                  offsets: torch.Tensor | None = None, codes: torch.Tensor | None = None,
-                 scales: torch.Tensor | None = None):
+                 scales: torch.Tensor | None = None, stream=None):
     """A 2-D (M, K) view to microscaled fp4 (fmt CK_MXFP4 or CK_NVFP4); returns (codes uint8
     (M, K/2) with rows at a pitch of 16 bytes, scales uint8 in tiles).  offsets (n_experts + 1 int32
     on the device): rows sorted by expert, each expert's scales in tiles of its own."""
+    if stream is not None:
+        return _on_stream(stream, x, ck_quant_fp4, x, fmt, tensor_scale=tensor_scale, offsets=offsets,
+                          codes=codes, scales=scales)
     M, K = x.shape
     _check_fp4(fmt, K)
     dt = _float_code(x, "x")
@@ -523,19 +522,21 @@ def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None
     else:
         _check_scales(scales, "scales", nbytes)
     sm, sk = x.stride()
-    st = _launch(lib().ck_quant_fp4, dev, (
+    _launch("ck_quant_fp4", dev, (
         x.data_ptr(), dt, M, K, sm, sk, fmt, None if tensor_scale is None else tensor_scale.data_ptr(),
         None if offsets is None else offsets.data_ptr(), E, codes.data_ptr(),
         max(codes.stride(0), half), scales.data_ptr()))
-    _check(st, "ck_quant_fp4")
     return codes, scales
 
 
-@_on_stream
 def ck_dequant_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: int, *,
                    tensor_scale: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
-                   out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+                   out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                   stream=None) -> torch.Tensor:
     """The values that codes (M, K/2) and their scale tiles stand for, (M, K)."""
+    if stream is not None:
+        return _on_stream(stream, codes, ck_dequant_fp4, codes, scales, fmt, tensor_scale=tensor_scale,
+                          offsets=offsets, out=out, out_dtype=out_dtype)
     M, half = codes.shape
     K = 2 * half
     _check_fp4(fmt, K)
@@ -550,17 +551,19 @@ def ck_dequant_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: int, *,
     else:
         _check_out(out, M, K, codes)
     odt = _float_code(out, "out")
-    st = _launch(lib().ck_dequant_fp4, dev, (
+    _launch("ck_dequant_fp4", dev, (
         codes.data_ptr(), max(codes.stride(0), half), scales.data_ptr(), M, K, fmt,
         None if tensor_scale is None else tensor_scale.data_ptr(),
         None if offsets is None else offsets.data_ptr(), E, out.data_ptr(), odt, max(out.stride(0), K)))
-    _check(st, "ck_dequant_fp4")
     return out
 
 
 def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_scale, w_tensor_scale,
-                 out, out_dtype, workspace, dev_status):
+                 out, out_dtype, workspace, dev_status, stream):
     """Both products: E weight matrices w of N channels; offsets None for the plain linear."""
+    if stream is not None:
+        return _on_stream(stream, x, _fp4_product, x, offsets, w, E, N, w_scales, fmt, bias, x_scales,
+                          x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status, None)
     M, K = x.shape
     dt = _FLOAT_CODE.get(x.dtype)
     if dt is None:
@@ -572,7 +575,8 @@ def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_sc
                      workspace, dev_status)
     half = K // 2
     nE = 0 if offsets is None else E
-    if w.shape[-1] != half or w.dtype != torch.uint8 or w.stride(-1) != 1:
+    w_strides = w.stride()
+    if w.shape[-1] != half or w.dtype != torch.uint8 or w_strides[-1] != 1:
         raise ValueError(f"w_codes must be uint8 of {half} bytes a row with unit inner stride; got "
                          f"{tuple(w.shape)} {w.dtype} strides {w.stride()}")
     per = fp4_scales_bytes(N, K, fmt)
@@ -613,41 +617,40 @@ def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_sc
         if out_dtype is None:
             out_dtype = x.dtype if dt != CK_FP4 else torch.bfloat16 if bias is None else bias.dtype
         out = torch.empty(M, N, dtype=out_dtype, device=x.device)
+        ldo = N
     else:
         _check_out(out, M, N, x)
+        ldo = max(out.stride(0), N)
     odt = _float_code(out, "out")
     head = (x.data_ptr(), dt, M, K, sm, sk, fmt, None if x_scales is None else x_scales.data_ptr(),
             None if x_tensor_scale is None else x_tensor_scale.data_ptr())
     tail = (w_scales.data_ptr(), None if w_tensor_scale is None else w_tensor_scale.data_ptr(),
-            None if bias is None else bias.data_ptr(), bdt, out.data_ptr(), odt, max(out.stride(0), N),
+            None if bias is None else bias.data_ptr(), bdt, out.data_ptr(), odt, ldo,
             ws, wsb, None if dev_status is None else dev_status.data_ptr())
-    w_ld = max(w.stride(-2), half)
+    w_ld = max(w_strides[-2], half)
     if nE:
-        st = _launch(lib().ck_fp4_expert_linear, dev, (
-            *head, offsets.data_ptr(), E, w.data_ptr(), N, w_ld, w.stride(0), *tail))
+        _launch("ck_fp4_expert_linear", dev, (
+            *head, offsets.data_ptr(), E, w.data_ptr(), N, w_ld, w_strides[0], *tail))
     else:
-        st = _launch(lib().ck_fp4_linear, dev, (*head, w.data_ptr(), N, w_ld, *tail))
-    _check(st, "ck_fp4_expert_linear" if nE else "ck_fp4_linear")
+        _launch("ck_fp4_linear", dev, (*head, w.data_ptr(), N, w_ld, *tail))
     return out
 
 
-@_on_stream
 def ck_fp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, fmt: int,
                   bias: torch.Tensor | None = None, *, x_scales: torch.Tensor | None = None,
                   x_tensor_scale: torch.Tensor | None = None,
                   w_tensor_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
                   out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
-                  dev_status: torch.Tensor | None = None) -> torch.Tensor:
+                  dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The linear on microscaled fp4: x (M, K) activations (quantized on the way), or uint8 codes
     (M, K/2) with x_scales; w_codes (N, K/2) and w_scales as ck_quant_fp4 returns them.  Returns
     out (M, N)."""
     if w_codes.dim() != 2:
         raise ValueError(f"w_codes must be (N, K/2); got {tuple(w_codes.shape)}")
     return _fp4_product(x, None, w_codes, 1, w_codes.shape[0], w_scales, fmt, bias, x_scales,
-                        x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status)
+                        x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status, stream)
 
 
-@_on_stream
 def ck_fp4_expert_linear(x: torch.Tensor, offsets: torch.Tensor, w_codes: torch.Tensor,
                          w_scales: torch.Tensor, fmt: int, bias: torch.Tensor | None = None, *,
                          x_scales: torch.Tensor | None = None,
@@ -655,7 +658,7 @@ def ck_fp4_expert_linear(x: torch.Tensor, offsets: torch.Tensor, w_codes: torch.
                          w_tensor_scale: torch.Tensor | None = None,
                          out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                          workspace: torch.Tensor | None = None,
-                         dev_status: torch.Tensor | None = None) -> torch.Tensor:
+                         dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """ck_fp4_linear with rows sorted by expert: rows [offsets[e], offsets[e+1]) of x times
     w_codes[e] (n_experts, N, K/2) with w_scales[e] (n_experts, bytes), w_tensor_scale[e] and
     bias[e].  offsets stays on the device; rows of no expert keep what `out` held."""
@@ -663,4 +666,5 @@ def ck_fp4_expert_linear(x: torch.Tensor, offsets: torch.Tensor, w_codes: torch.
         raise ValueError("offsets must be given, and w_codes be (n_experts, N, K/2); got "
                          f"{tuple(w_codes.shape)}")
     return _fp4_product(x, offsets, w_codes, w_codes.shape[0], w_codes.shape[1], w_scales, fmt, bias,
-                        x_scales, x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status)
+                        x_scales, x_tensor_scale, w_tensor_scale, out, out_dtype, workspace, dev_status,
+                        stream)

@@ -66,7 +66,6 @@ struct Fp4GemmParams {
     int num_kb;           // stages per tile: ceil(K / 256)
     int k64;              // MMA steps per tile: ceil(K / 64)
     int BN;               // rows per tile
-    int nblk;             // 128-row scale blocks a tile's rows may touch
     int tiles_n;          // tiles along the channels
     int stages;
     uint32_t b_bytes;     // a CTA's codes of the rows per stage
@@ -195,7 +194,7 @@ __device__ __forceinline__ void epilogue_any(uint32_t taddr, float alpha, float 
     }
 }
 
-template <typename OutT, bool NV, int CG, int NBLK>
+template <typename OutT, bool NV, int CG>
 __global__ void __launch_bounds__(fp4g::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap xmap,
                     const __grid_constant__ CUtensorMap wmap,
@@ -203,6 +202,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
                     const __grid_constant__ CUtensorMap wsmap, Fp4GemmParams p) {
     using namespace fp4g;
     constexpr int SF_TILES = NV ? 4 : 2;     // scale tiles per stage and 128 rows
+    constexpr int NBLK = CG;                 // 128-row scale blocks a tile's rows touch: pairs take 192
     constexpr uint32_t SFA_BYTES = SF_TILES * kFp4TileBytes, SFB_BYTES = NBLK * SFA_BYTES;
     extern __shared__ __align__(1024) unsigned char fp4_smem[];
     unsigned char* ring = reinterpret_cast<unsigned char*>(
@@ -513,13 +513,16 @@ struct Fp4Shape {
     int cg, bn;
 };
 
-// CTAs per tile and rows per tile, by the estimated time of the busiest unit: waves of tiles, each
-// the larger of its MMA time (BN / 2 cycles per 64 k: both SMs of a pair at 16384 multiply-adds a
-// cycle each; BN for... one SM has half the pair's rate on half the channels, the same time) and the
-// time its bytes take to arrive at about 64 bytes a cycle and SM, plus a fixed cost.
+// CTAs per tile and rows per tile, by the estimated cycles of the busiest unit.  A stage takes its
+// MMAs and scale copies (BN / 2 cycles per 64 k, 14 per copy) but never less than about 520, what its
+// waits and issues take; a tile a little more; the last tile's epilogue about 30 a row, and a pair
+// about 2500 more to start and end.  Measured, us: 413 x 2064 x 1111 NV (one wave each): 13.0, 10.3, 8.3
+// with {2, 192}, {1, 128}, {1, 64}; 8192 x 3840 x 3840 NV: 55.5, 66.7, 118; 64 rows over 32 experts,
+// 3840 x 3840 MX (HBM-bound): 38, 43, 32.  Pairs of 128 rows were never the best by more than 2%.
+// Tiles start at multiples of 64 rows, so that a tile's first scale column is even; 32 rows only where
+// one tile holds them all.
 static Fp4Shape choose_shape(int64_t M, int64_t N, int64_t num_kb, int n_experts, int sms) {
-    // 64-row steps keep a tile's first scale column even; 32 rows only where one tile holds them all
-    static const Fp4Shape all[] = {{2, 192}, {2, 128}, {1, 128}, {1, 64}, {1, 32}};
+    static const Fp4Shape all[] = {{2, 192}, {1, 128}, {1, 64}, {1, 32}};
     const int64_t m = (M + n_experts - 1) / n_experts;   // rows of an expert, were they even
     Fp4Shape best = all[0];
     double best_cost = -1.0;
@@ -528,10 +531,9 @@ static Fp4Shape choose_shape(int64_t M, int64_t N, int64_t num_kb, int n_experts
         const int64_t units = sms / s.cg;
         const int64_t tiles = (int64_t)n_experts * ((m + s.bn - 1) / s.bn) *
                               ((N + 128 * s.cg - 1) / (128 * s.cg));
-        const double mma = 4.0 * s.bn / 2;
-        const double load = (128.0 * 128 + 128.0 * s.bn / s.cg + 6144) / 64;
-        const double tile = (double)num_kb * (mma > load ? mma : load) + 600.0;
-        const double cost = (double)((tiles + units - 1) / units) * tile;
+        const double stage = 2.0 * s.bn + (s.bn > 128 ? 168.0 : 112.0);
+        const double tile = (double)num_kb * (stage > 520.0 ? stage : 520.0) + 600.0;
+        const double cost = (double)((tiles + units - 1) / units) * tile + 30.0 * s.bn + (s.cg == 2 ? 2500.0 : 0.0);
         if (best_cost < 0 || cost < best_cost) {
             best_cost = cost;
             best = s;
@@ -540,10 +542,10 @@ static Fp4Shape choose_shape(int64_t M, int64_t N, int64_t num_kb, int n_experts
     return best;
 }
 
-template <typename OutT, bool NV, int CG, int NBLK>
+template <typename OutT, bool NV, int CG>
 static ck_status fp4_launch(const CUtensorMap* maps, const Fp4GemmParams& p, size_t smem, int grid,
                             bool dep, cudaStream_t stream) {
-    auto kern = fp4_gemm_kernel<OutT, NV, CG, NBLK>;
+    auto kern = fp4_gemm_kernel<OutT, NV, CG>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return CK_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -575,14 +577,11 @@ static ck_status fp4_launch(const CUtensorMap* maps, const Fp4GemmParams& p, siz
 template <typename OutT>
 static ck_status fp4_launch_out(const CUtensorMap* maps, const Fp4GemmParams& p, size_t smem, int grid,
                                 bool nv, int cg, bool dep, cudaStream_t stream) {
-    const bool two = p.nblk == 2;   // BN = 192, which only pairs take
     if (nv)
-        return cg == 1 ? fp4_launch<OutT, true, 1, 1>(maps, p, smem, grid, dep, stream)
-               : two   ? fp4_launch<OutT, true, 2, 2>(maps, p, smem, grid, dep, stream)
-                       : fp4_launch<OutT, true, 2, 1>(maps, p, smem, grid, dep, stream);
-    return cg == 1 ? fp4_launch<OutT, false, 1, 1>(maps, p, smem, grid, dep, stream)
-           : two   ? fp4_launch<OutT, false, 2, 2>(maps, p, smem, grid, dep, stream)
-                   : fp4_launch<OutT, false, 2, 1>(maps, p, smem, grid, dep, stream);
+        return cg == 2 ? fp4_launch<OutT, true, 2>(maps, p, smem, grid, dep, stream)
+                       : fp4_launch<OutT, true, 1>(maps, p, smem, grid, dep, stream);
+    return cg == 2 ? fp4_launch<OutT, false, 2>(maps, p, smem, grid, dep, stream)
+                   : fp4_launch<OutT, false, 1>(maps, p, smem, grid, dep, stream);
 }
 
 ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream) {
@@ -598,12 +597,11 @@ ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream) {
     p.num_kb = (int)num_kb;
     p.k64 = (int)((a.K + 63) / 64);
     p.BN = shape.bn;
-    p.nblk = shape.bn > 128 ? 2 : 1;
     p.tiles_n = (int)((a.N + BW * shape.cg - 1) / (BW * shape.cg));
     // the tile count stays an int: rows split over experts give at most one more tile each
     if ((double)p.tiles_n * ((double)a.M / p.BN + E + 1) >= 2147483647.0) return CK_ERR_UNSUPPORTED;
     p.b_bytes = (uint32_t)(shape.bn / shape.cg) * (BK / 2);
-    const uint32_t sf_bytes = (a.nv ? 4 : 2) * kFp4TileBytes * (1 + p.nblk);
+    const uint32_t sf_bytes = (a.nv ? 4 : 2) * kFp4TileBytes * (1 + shape.cg);
     p.stage_bytes = (A_BYTES + p.b_bytes + sf_bytes + 1023) & ~1023u;
     const size_t fixed = 1024 + EPI_WARPS * EPI_STAGE_BYTES + (size_t)(E + 1) * sizeof(int);
     p.stages = (int)((SMEM_MAX - fixed) / p.stage_bytes);
@@ -645,7 +643,7 @@ ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream) {
     {
         const uint64_t dims[3] = {tile_words, (uint64_t)k_tiles, sf_blocks};
         const uint64_t strides[2] = {kFp4TileBytes, (uint64_t)k_tiles * kFp4TileBytes};
-        const uint32_t box[3] = {(uint32_t)tile_words, sf_tiles, (uint32_t)p.nblk};
+        const uint32_t box[3] = {(uint32_t)tile_words, sf_tiles, (uint32_t)shape.cg};
         const ck_status st = encode_tma(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, a.scales, dims, strides,
                                         box, CU_TENSOR_MAP_SWIZZLE_NONE);
         if (st != CK_OK) return st;

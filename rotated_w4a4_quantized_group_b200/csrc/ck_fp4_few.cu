@@ -14,6 +14,9 @@
 //   - multiplies on the tensor cores, 128 channels x BN rows, as the weights arrive,
 //   - writes its partial sums to shared memory; after a cluster barrier each CTA adds its share of
 //     the tile over the S partials in rank order (no atomics) and stores it.
+// Measured, 3840 x 3840: one bf16 row to NV 7.0 us replayed back to back (10.2 with the quantizer and
+// the persistent kernel), 32 rows with the quantizer before it 7.5 (10.1); the weights alone are 1.3 us
+// of HBM.
 // Every CTA takes both cluster barriers whatever happened before them; every mbarrier wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -18,6 +18,9 @@
 //            MMAs that read them) and issues the MMAs: the CTA of rank 0 for both CTAs
 //   warps 4-11  the epilogue: two warps per lane quarter on alternate 32-row chunks, from one of
 //            two accumulators while the MMAs fill the other
+// Measured (graph-replayed, the product alone): 8192 x 3840 x 3840 NV 54.8 us (4.4 PFLOP/s; tensor pipe
+// 60% of active cycles, 1.63 GHz at the power cap), 8192 x 10240 x 3840 MX 116 us (5.5 PFLOP/s); a stage
+// takes 547 (NV) or 476 (MX) cycles where its MMAs alone need 384.
 // Every wait is bounded; a CTA leaves only after its own copies have landed, the MMAs that read
 // its memory have completed and the arrivals that were sent to it have come.
 #include <cuda.h>

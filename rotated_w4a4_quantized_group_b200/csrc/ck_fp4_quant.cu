@@ -4,7 +4,10 @@
 //               code = e2m1(x / scale); see ck_fp4.cuh for the arithmetic of one block
 //   dequantize: value = cvt(fl(fl(code * scale) * t))
 //
-// Both are one pass over memory, bound by HBM: K * sizeof(x) + K / 2 + K / block bytes a row.
+// Both are one pass over memory: K * sizeof(x) + K / 2 + K / block bytes a row, 12.5 us for 8192 x 3840
+// bf16 at the measured copy rate.  Measured there: MX 15.2 us, NV with a tensor scale 19.3 (about 206
+// instructions a thread and block, of them 50 for the scale: the integer pipe is 61% busy), back 13.9;
+// 4096 x 16384 fp32: NV 52 us (48 at the copy rate), column-major 74, back 51.
 // A CTA takes 128 rows x 128 channels, so that it owns whole 512-byte scale tiles and writes each
 // of them as one contiguous run from shared memory; a thread takes sixteen channels of a row (an
 // NV block, or half an MX block whose other half is its neighbour lane's), with the loads of

@@ -602,7 +602,8 @@ def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_sc
         if x_scales is None:
             raise ValueError("x holds fp4 codes: x_scales must be given")
         _check_scales(x_scales, "x_scales", fp4_scales_bytes(M, K, fmt, nE))
-        sm, sk = max(sm, half), 1
+        # one row's pitch is never used, and need not be one that TMA could
+        sm, sk = (max(sm, half) if M > 1 else (half + 15) // 16 * 16), 1
     else:
         x_scales = None
         if workspace is None:
@@ -627,7 +628,7 @@ def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_sc
     tail = (w_scales.data_ptr(), None if w_tensor_scale is None else w_tensor_scale.data_ptr(),
             None if bias is None else bias.data_ptr(), bdt, out.data_ptr(), odt, ldo,
             ws, wsb, None if dev_status is None else dev_status.data_ptr())
-    w_ld = max(w_strides[-2], half)
+    w_ld = max(w_strides[-2], half) if N > 1 else (half + 15) // 16 * 16
     if nE:
         _launch("ck_fp4_expert_linear", dev, (
             *head, offsets.data_ptr(), E, w.data_ptr(), N, w_ld, w_strides[0], *tail))

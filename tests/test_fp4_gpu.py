@@ -582,6 +582,55 @@ def test_captured_expert_call_follows_its_offsets(fmt):
 
 
 @FMT
+def test_one_row_and_one_channel_at_any_pitch(fmt):
+    """A single row of codes, or a single channel's weights, needs no 16-byte pitch."""
+    K = 96                                                       # 48 bytes a row
+    x, w, ws = _case(fmt, 5, 1, K)
+    want = ck.ck_fp4_linear(x, w, ws, fmt)
+    tight = w.contiguous().clone()
+    assert torch.equal(ck.ck_fp4_linear(x, tight, ws, fmt), want)
+    codes, scales = ck.ck_quant_fp4(x[:1], fmt)
+    for c in (codes, codes.contiguous().clone(), codes.expand(1, K // 2).clone()):
+        assert torch.equal(ck.ck_fp4_linear(c, tight, ws, fmt, x_scales=scales), want[:1])
+
+
+@FMT
+def test_as_many_experts_as_a_call_takes(fmt):
+    E, N, K = 1024, 40, 64
+    g = torch.Generator().manual_seed(8)
+    count = torch.randint(0, 4, (E,), generator=g)
+    off = torch.cat([count.new_zeros(1), count.cumsum(0)]).int()
+    M = int(off[-1])
+    x = _x(M, K, BF16, 31, spread=False)
+    wc = torch.randint(0, 256, (E, N, K // 2), generator=g, dtype=torch.uint8)
+    byte = np.random.default_rng(9).integers(*((120, 130) if fmt == MX else (40, 80)),
+                                             (E, N, K // ref.BLOCK[fmt])).astype(np.uint8)
+    ws = torch.from_numpy(np.stack([ref.tile(b) for b in byte])).cuda()
+    out = ck.ck_fp4_expert_linear(x.cuda(), off.cuda(), wc.cuda(), ws, fmt)
+    xv = _xvalues(x, fmt, None)
+    wv = torch.from_numpy(ref.values(ref.unpack(wc.numpy()), byte, fmt)).cuda()
+    w_of = wv[torch.repeat_interleave(torch.arange(E), count).cuda()]
+    exact, mag = (xv[:, None] * w_of).sum(-1), (xv[:, None] * w_of).abs().sum(-1)
+    _close(out, exact, mag, K)
+    with pytest.raises(ck.CkError):
+        two = torch.cat([off, off[-1:]]).cuda()
+        ck.ck_fp4_expert_linear(x.cuda(), two, torch.cat([wc, wc[:1]]).cuda(), torch.cat([ws, ws[:1]]), fmt)
+
+
+@FMT
+def test_the_default_stream_by_its_handle(fmt):
+    x, w, ws = _case(fmt, 40, 64, 128)
+    want = ck.ck_fp4_linear(x, w, ws, fmt)
+    torch.cuda.synchronize()
+    for s in (0, torch.cuda.default_stream(), torch.cuda.default_stream().cuda_stream):
+        codes, scales = ck.ck_quant_fp4(x, fmt, stream=s)
+        got = ck.ck_fp4_linear(codes, w, ws, fmt, x_scales=scales, stream=s)
+        ck.ck_dequant_fp4(codes, scales, fmt, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+@FMT
 @pytest.mark.parametrize("M", [12, 48, 400])
 def test_two_calls_at_once_on_two_streams(fmt, M):
     x, w, ws = _case(fmt, M, 1000, 2080)

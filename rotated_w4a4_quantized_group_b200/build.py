@@ -5,7 +5,8 @@
 Compiles every csrc/*.cu with nvcc for sm_100a and links them into one shared
 library exporting the C ABI declared in include/ck.h.  It also builds
 libck_test_waits.so, the same sources with every role wait limited to zero cycles,
-which the bounded-wait expiry test loads to drive each kernel through its timeout path.
+which the bounded-wait expiry test loads to drive each kernel through its timeout path, and
+_ck_bind.so, the host side of the fp4 calls (csrc/ck_bind.cpp, against torch's headers).
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -84,8 +86,36 @@ def build(force: bool = False, variant=None) -> str:
     return lib
 
 
+BIND_SRC = os.path.join(CSRC, "ck_bind.cpp")
+BIND = os.path.join(HERE, "_ck_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def build_bind(force: bool = False) -> str:
+    """The Python extension _ck_bind, which loads libck.so when it is told where."""
+    deps = [BIND_SRC, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(BIND) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(BIND) for p in deps):
+        return BIND
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(t, "include"),
+           "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(cuda, "include"), BIND_SRC, "-o", tmp, "-L" + os.path.join(t, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build_all(force: bool = False) -> list:
-    return [build(force, v) for v in VARIANTS]
+    return [build(force, v) for v in VARIANTS] + [build_bind(force)]
 
 
 if __name__ == "__main__":

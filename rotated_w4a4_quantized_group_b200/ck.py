@@ -66,6 +66,7 @@ class CkError(RuntimeError):
 
 
 _lib = None
+_bind = None      # the native host side of the fp4 calls, once libck.so is loaded
 
 
 def load_library(path: str) -> ctypes.CDLL:
@@ -83,9 +84,16 @@ def load_library(path: str) -> ctypes.CDLL:
 
 def lib() -> ctypes.CDLL:
     """Load libck.so (raises if it is missing: build it with the package's build module)."""
-    global _lib
+    global _lib, _bind
     if _lib is None:
         _lib = load_library(LIB_PATH)
+        try:
+            from . import _ck_bind
+        except ImportError:     # not built: the fp4 calls take Python's way, with the same results
+            pass
+        else:
+            _ck_bind.load(LIB_PATH)
+            _bind = _ck_bind
     return _lib
 
 
@@ -401,9 +409,11 @@ def ck_unpack_w4(packed: torch.Tensor, K: int, out: torch.Tensor | None = None,
 
 # ------------------------------------------------------------------ microscaled fp4
 #
-# A small call's time is mostly the host's, so these functions check each tensor once and with the
-# cheapest accessors (get_device() is -1 for a host tensor), and enter a device context only when
-# another device is current.
+# A small call's time is mostly the host's.  Usual calls go through _ck_bind, which does what the code
+# here does in a fifth of the time and declines (None) whatever it has any objection to; the code here
+# then says what is wrong, or handles it.  It checks each tensor once and with the cheapest accessors
+# (get_device() is -1 for a host tensor), and enters a device context only when another device is
+# current.
 
 @functools.lru_cache(maxsize=4096)
 def fp4_scales_bytes(M: int, K: int, fmt: int, n_experts: int = 0) -> int:
@@ -440,7 +450,7 @@ def _on_stream(stream, like: torch.Tensor, fn, *args, **kw):
 
 def _launch(name: str, dev: int, args):
     """The library's `name` on torch's current stream of `dev`, with `dev` current."""
-    fn = getattr(_lib or lib(), name)
+    fn = getattr(lib(), name)
     if dev == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
@@ -448,6 +458,13 @@ def _launch(name: str, dev: int, args):
             st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != CK_OK:
         raise CkError(st, name)
+
+
+def _bound(r, name: str):
+    """The result of a _ck_bind call: a status of the library is raised."""
+    if r.__class__ is int:
+        raise CkError(r, name)
+    return r
 
 
 def _check_fp4(fmt: int, K: int):
@@ -499,6 +516,10 @@ def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None
     """A 2-D (M, K) view to microscaled fp4 (fmt CK_MXFP4 or CK_NVFP4); returns (codes uint8
     (M, K/2) with rows at a pitch of 16 bytes, scales uint8 in tiles).  offsets (n_experts + 1 int32
     on the device): rows sorted by expert, each expert's scales in tiles of its own."""
+    if _bind is not None and stream is None:
+        r = _bind.quant(x, fmt, tensor_scale, offsets, codes, scales)
+        if r is not None:
+            return _bound(r, "ck_quant_fp4")
     if stream is not None:
         return _on_stream(stream, x, ck_quant_fp4, x, fmt, tensor_scale=tensor_scale, offsets=offsets,
                           codes=codes, scales=scales)
@@ -534,6 +555,10 @@ def ck_dequant_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: int, *,
                    out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
                    stream=None) -> torch.Tensor:
     """The values that codes (M, K/2) and their scale tiles stand for, (M, K)."""
+    if _bind is not None and stream is None and out is None:
+        r = _bind.dequant(codes, scales, fmt, tensor_scale, offsets, out_dtype)
+        if r is not None:
+            return _bound(r, "ck_dequant_fp4")
     if stream is not None:
         return _on_stream(stream, codes, ck_dequant_fp4, codes, scales, fmt, tensor_scale=tensor_scale,
                           offsets=offsets, out=out, out_dtype=out_dtype)
@@ -646,6 +671,11 @@ def ck_fp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor
     """The linear on microscaled fp4: x (M, K) activations (quantized on the way), or uint8 codes
     (M, K/2) with x_scales; w_codes (N, K/2) and w_scales as ck_quant_fp4 returns them.  Returns
     out (M, N)."""
+    if _bind is not None and stream is None:
+        r = _bind.product(x, None, w_codes, w_scales, fmt, bias, x_scales, x_tensor_scale, w_tensor_scale,
+                          out, out_dtype, workspace, dev_status)
+        if r is not None:
+            return _bound(r, "ck_fp4_linear")
     if w_codes.dim() != 2:
         raise ValueError(f"w_codes must be (N, K/2); got {tuple(w_codes.shape)}")
     return _fp4_product(x, None, w_codes, 1, w_codes.shape[0], w_scales, fmt, bias, x_scales,
@@ -663,6 +693,11 @@ def ck_fp4_expert_linear(x: torch.Tensor, offsets: torch.Tensor, w_codes: torch.
     """ck_fp4_linear with rows sorted by expert: rows [offsets[e], offsets[e+1]) of x times
     w_codes[e] (n_experts, N, K/2) with w_scales[e] (n_experts, bytes), w_tensor_scale[e] and
     bias[e].  offsets stays on the device; rows of no expert keep what `out` held."""
+    if _bind is not None and stream is None and offsets is not None:
+        r = _bind.product(x, offsets, w_codes, w_scales, fmt, bias, x_scales, x_tensor_scale,
+                          w_tensor_scale, out, out_dtype, workspace, dev_status)
+        if r is not None:
+            return _bound(r, "ck_fp4_expert_linear")
     if offsets is None or w_codes.dim() != 3:
         raise ValueError("offsets must be given, and w_codes be (n_experts, N, K/2); got "
                          f"{tuple(w_codes.shape)}")

@@ -805,3 +805,85 @@ def test_wait_expiry_returns_a_status(fmt, what, M, N, K, E):
         xv = _xvalues(x[:100].cpu(), fmt, None)
         _close(good[:100], xv @ wv[0].t(), xv.abs() @ wv[0].abs().t(), K, what)
     assert status.item() == 0
+
+
+# ------------------------------------------------------------------- both host sides
+
+def _forms():
+    """Call forms, sound ones and ones that are refused."""
+    x, w, ws = _case(NV, 40, 200, 544)
+    w3, ws3, _ = _weights(3, 64, 544, NV, 95)
+    t, tw3 = _t(0.07), torch.tensor([0.1, 0.2, 0.3], device="cuda")
+    off = torch.tensor([0, 10, 10, 35], dtype=torch.int32, device="cuda")
+    codes, scales = ck.ck_quant_fp4(x, NV)
+    ecodes, escales = ck.ck_quant_fp4(x, NV, offsets=off)
+    bias, bias3 = torch.randn(200, device="cuda"), torch.randn(3, 64, device="cuda").half()
+    work = torch.empty(ck.fp4_workspace_bytes(40, 544, NV), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    L, X, Q, D = ck.ck_fp4_linear, ck.ck_fp4_expert_linear, ck.ck_quant_fp4, ck.ck_dequant_fp4
+
+    def into(fn, shape, dt, *a, **kw):
+        out = torch.full(shape, -3.0, dtype=dt, device="cuda")
+        assert fn(*a, out=out, **kw) is out
+        return out
+
+    good = [
+        lambda: Q(x, NV), lambda: Q(x, NV, tensor_scale=t), lambda: Q(x.float(), MX), lambda: Q(x[:0], NV),
+        lambda: Q(x[:, :528], NV), lambda: Q(x[:1].half(), NV), lambda: Q(x[:, ::2], NV),
+        lambda: D(codes, scales, NV), lambda: D(codes, scales, NV, tensor_scale=t, out_dtype=F32),
+        lambda: D(codes[:1], scales, NV, out_dtype=F16), lambda: D(codes[:0], scales, NV),
+        lambda: L(x, w, ws, NV), lambda: L(x[:1], w, ws, NV, bias), lambda: L(x[:0], w, ws, NV),
+        lambda: L(x.float(), w, ws, NV, bias.bfloat16(), x_tensor_scale=t, w_tensor_scale=t),
+        lambda: L(codes, w, ws, NV, x_scales=scales), lambda: L(codes, w, ws, NV, bias, x_scales=scales),
+        lambda: L(codes[:1], w, ws, NV, x_scales=scales, out_dtype=F16), lambda: L(x, w[:1], ws, NV),
+        lambda: L(x, w, ws, NV, workspace=work, dev_status=status), lambda: L(x, w, ws, NV, out_dtype=F32),
+        lambda: into(L, (40, 200), F16, x, w, ws, NV), lambda: L(x.t().contiguous().t(), w, ws, NV),
+        lambda: into(X, (40, 64), F32, x, off, w3, ws3, NV, bias3, w_tensor_scale=tw3),
+        lambda: into(X, (40, 64), BF16, ecodes, off, w3, ws3, NV, x_scales=escales, x_tensor_scale=t),
+    ]
+    refused = [
+        lambda: L(x, w[:, :16], ws, NV), lambda: L(x, w, ws[:-16], NV), lambda: L(x, w, ws, 9),
+        lambda: L(x, w, ws, NV, bias[:-1]), lambda: L(x, w, ws, MX, x_tensor_scale=t),
+        lambda: L(codes, w, ws, NV), lambda: L(x, w, ws, NV, out_dtype=torch.int32), lambda: L(x, w3, ws3, NV),
+        lambda: L(x.cpu(), w, ws, NV), lambda: L(x, w, ws.cpu(), NV), lambda: L(x.int(), w, ws, NV),
+        lambda: L(x, w, ws, NV, workspace=work[:-256]), lambda: L(x, w, ws, NV, out=bias),
+        lambda: X(x, off.long(), w3, ws3, NV), lambda: X(x, off[:3], w3, ws3, NV), lambda: X(x, off, w, ws, NV),
+        lambda: X(x, None, w3, ws3, NV), lambda: X(x, off, w3, ws3.flatten(), NV), lambda: Q(x[:, :40], NV),
+        lambda: Q(x[0], NV), lambda: Q(x, NV, tensor_scale=t.double()), lambda: D(codes.char(), scales, NV),
+        lambda: D(codes, scales[:-16], NV), lambda: D(codes, scales, NV, out_dtype=torch.int32),
+    ]
+    return good, refused
+
+
+def test_native_and_python_host_sides_agree(monkeypatch):
+    """The native host side takes every ordinary call, gives the bits that Python's way gives, and
+    refuses what Python's way refuses, with its words."""
+    assert ck._bind is not None, "_ck_bind is not built"
+    good, refused = _forms()
+    native = [f() for f in good]
+    errors = []
+    for f in refused:
+        with pytest.raises(Exception) as e:
+            f()
+        errors.append(e)
+    monkeypatch.setattr(ck, "_bind", None)
+    for i, (f, n) in enumerate(zip(good, native)):
+        p = f()
+        for a, b in zip(n, p) if isinstance(p, tuple) else ((n, p),):
+            assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(
+                a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)), f"form {i}"
+    for i, (f, e) in enumerate(zip(refused, errors)):
+        with pytest.raises(type(e.value)) as again:
+            f()
+        assert str(again.value) == str(e.value), f"refused form {i}"
+
+
+def test_native_host_side_takes_ordinary_calls():
+    x, w, ws = _case(NV, 20, 64, 128)
+    codes, scales = ck._bind.quant(x, NV, None, None, None, None)
+    assert isinstance(ck._bind.dequant(codes, scales, NV, None, None, BF16), torch.Tensor)
+    out = ck._bind.product(x, None, w, ws, NV, None, None, None, None, None, None, None, None)
+    assert torch.equal(out, ck.ck_fp4_linear(x, w, ws, NV))
+    for bad in [(x.cpu(), NV), (x, 7), (x, None), (None, NV), (x.int(), NV), (x[:, :24], NV)]:
+        assert ck._bind.quant(*bad, None, None, None, None) is None
+    assert ck._bind.quant() is None and ck._bind.product(x) is None

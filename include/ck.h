@@ -334,8 +334,9 @@ ck_status ck_dequant_fp4(const uint8_t* codes, int64_t ldq, const uint8_t* scale
  *   workspace, workspace_bytes
  *             for floating-point x: at least ck_fp4_linear_workspace_bytes(M, K, format, 0) bytes of
  *             device scratch, 256-byte aligned: the codes (row pitch K / 2 rounded up to 16), then,
- *             256-byte aligned, the scale tiles.  Not used for CK_FP4, nor where that size is 0: up to
- *             16 rows (K up to about 16,000) are quantized inside the product's kernel.
+ *             256-byte aligned, the scale tiles.  Not used for CK_FP4, nor where that size is 0: few
+ *             values (at most 16 rows, M * ceil(K / 256) <= 180) are quantized inside the product's
+ *             kernel.
  * Errors: CK_ERR_INVALID_ARG, CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (a size of 2^31 or more, or as
  * many tiles; more than 8,388,480 channels with at most 64 rows), CK_ERR_CUDA.
  */

@@ -5,12 +5,13 @@
 //
 // 128-channel tiles alone would be N / 128 CTAs, so each tile's K is split over a cluster of S CTAs
 // (S * N / 128 about one per SM), each of which
-//   - asks for its whole share of the weights at once (one box of codes and one of scale tiles per
-//     256 k, each pair on its own mbarrier),
+//   - asks for its share of the weights, as many steps of 256 k at once as shared memory holds (one
+//     box of codes and one of scale tiles a step, on the step's mbarrier), for the others as MMAs
+//     free their slots,
 //   - meanwhile, FUSED, quantizes the rows' share of K straight into the shared-memory layouts that
-//     the MMA and the scale copies read (up to 16 rows: one launch, no workspace; every tile repeats
-//     the quantizing, which with more rows costs more than the launch saved), or else loads codes
-//     and scales that the quantizer before it wrote,
+//     the MMA and the scale copies read (one launch, no workspace; every tile repeats the
+//     quantizing, so this is for few values: see fp4_few_fuses), or else loads codes and scales that
+//     the quantizer before it wrote,
 //   - multiplies on the tensor cores, 128 channels x BN rows, as the weights arrive,
 //   - writes its partial sums to shared memory; after a cluster barrier each CTA adds its share of
 //     the tile over the S partials in rank order (no atomics) and stores it.
@@ -35,10 +36,9 @@ namespace fp4f {
 constexpr int BW = 128;                  // channels per tile
 constexpr int BK = 256;                  // k per step of the ring: 128 bytes of codes
 constexpr int THREADS = 256;
-constexpr int KB_MAX = 8;                // steps of one CTA
+constexpr int SLOTS_MAX = 8;             // steps of weights in flight
 constexpr int MAX_CLUSTER = 8;
 constexpr uint32_t A_BYTES = BW * BK / 2;
-constexpr uint32_t SF_BYTES = 4 * kFp4TileBytes;   // scale tiles of 128 rows x 256 k, the NV size
 constexpr uint32_t TMEM_COLS = 128;
 constexpr uint32_t SF_COL = 64;          // accumulator [0, 64), then two sets of 16 + 16 scale columns
 constexpr size_t SMEM_BUDGET = 220 * 1024;
@@ -48,6 +48,7 @@ struct Fp4FewParams {
     int M, BN;               // rows, and the MMA's N
     int64_t N, K;
     int num_kb, kb_per;      // steps of K, and of one CTA
+    int slots;               // steps of weights (FUSED), or of both operands, held at a time
     uint32_t b_bytes;        // BN * 128
     uint32_t idesc;
     const void* x;           // FUSED: the activations
@@ -69,26 +70,28 @@ __device__ __forceinline__ float few_load(const void* p, ck_dtype dt, int64_t i)
     return load_scale<__nv_bfloat16>(p, i);
 }
 
-// T: the activations' type (FUSED), otherwise ignored.
-template <typename T, bool NV, bool HAS_T, bool FUSED>
+// T: the activations' type (FUSED), otherwise ignored.  RING: a CTA has more steps than slots (the short
+// form saves the smallest calls half a microsecond of 6.5).
+template <typename T, bool NV, bool HAS_T, bool FUSED, bool RING>
 __global__ void __launch_bounds__(fp4f::THREADS)
     fp4_few_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                    const __grid_constant__ CUtensorMap xsmap, const __grid_constant__ CUtensorMap wsmap,
                    Fp4FewParams p) {
     using namespace fp4f;
     constexpr int SF_TILES = NV ? 4 : 2;
-    constexpr uint32_t SF_USED = SF_TILES * kFp4TileBytes;
+    constexpr uint32_t SF_BYTES = SF_TILES * kFp4TileBytes;   // scale tiles of 128 rows x 256 k
     extern __shared__ __align__(1024) unsigned char few_smem[];
     unsigned char* abuf = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(few_smem) + 1023) & ~uintptr_t(1023));
-    unsigned char* bbuf = abuf + (size_t)p.kb_per * A_BYTES;
-    unsigned char* sfa_buf = bbuf + (size_t)p.kb_per * p.b_bytes;
-    unsigned char* sfb_buf = sfa_buf + (size_t)p.kb_per * SF_BYTES;
-    float* partial = reinterpret_cast<float*>(sfb_buf + (size_t)p.kb_per * SF_BYTES);   // [BN][128]
+    const int R = RING ? p.slots : p.kb_per, b_steps = FUSED ? p.kb_per : R;   // the rows' steps held
+    unsigned char* bbuf = abuf + (size_t)R * A_BYTES;
+    unsigned char* sfa_buf = bbuf + (size_t)b_steps * p.b_bytes;
+    unsigned char* sfb_buf = sfa_buf + (size_t)R * SF_BYTES;
+    float* partial = reinterpret_cast<float*>(sfb_buf + (size_t)b_steps * SF_BYTES);   // [BN][128]
 
-    __shared__ __align__(8) uint64_t full[KB_MAX], acc_full, drain_bar;
+    __shared__ __align__(8) uint64_t full[SLOTS_MAX], empty[SLOTS_MAX], acc_full, drain_bar;
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, loaded;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank(), ncta = cluster_nctarank();
@@ -96,26 +99,33 @@ __global__ void __launch_bounds__(fp4f::THREADS)
     const int n_kb = min(p.num_kb - kb_lo, p.kb_per);
     const int n0 = (int)blockIdx.y * BW;
 
+    auto load_w = [&](int i, int slot) {
+        mbar_arrive_expect_tx(&full[slot], A_BYTES + SF_BYTES);
+        tma_load_2d(abuf + (size_t)slot * A_BYTES, &wmap, &full[slot], (kb_lo + i) * (BK / 2), n0);
+        tma_load_3d(sfa_buf + (size_t)slot * SF_BYTES, &wsmap, &full[slot], 0, (kb_lo + i) * SF_TILES,
+                    (int)blockIdx.y);
+    };
+    auto load_x = [&](int i, int slot) {
+        mbar_arrive_expect_tx(&full[slot], p.b_bytes + SF_BYTES);
+        tma_load_2d(bbuf + (size_t)slot * p.b_bytes, &xmap, &full[slot], (kb_lo + i) * (BK / 2), 0);
+        tma_load_3d(sfb_buf + (size_t)slot * SF_BYTES, &xsmap, &full[slot], 0, (kb_lo + i) * SF_TILES, 0);
+    };
+    const int head = RING ? min(n_kb, R) : n_kb;   // steps asked for at once
     if (tid == 0) {
-        for (int i = 0; i < KB_MAX; ++i) mbar_init(&full[i], FUSED ? 1 : 2);
+        for (int i = 0; i < SLOTS_MAX; ++i) {
+            mbar_init(&full[i], FUSED ? 1 : 2);
+            if (RING) mbar_init(&empty[i], 1);
+        }
         mbar_init(&acc_full, 1);
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
+        loaded = head;
         fence_mbar_init();
         // the weights first: nothing else is as far away
-        for (int i = 0; i < n_kb; ++i) {
-            mbar_arrive_expect_tx(&full[i], A_BYTES + SF_USED);
-            tma_load_2d(abuf + (size_t)i * A_BYTES, &wmap, &full[i], (kb_lo + i) * (BK / 2), n0);
-            tma_load_3d(sfa_buf + (size_t)i * SF_BYTES, &wsmap, &full[i], 0, (kb_lo + i) * SF_TILES,
-                        (int)blockIdx.y);
-        }
+        for (int i = 0; i < head; ++i) load_w(i, i);
         if (!FUSED) {
             grid_dependency_wait();
-            for (int i = 0; i < n_kb; ++i) {
-                mbar_arrive_expect_tx(&full[i], p.b_bytes + SF_USED);
-                tma_load_2d(bbuf + (size_t)i * p.b_bytes, &xmap, &full[i], (kb_lo + i) * (BK / 2), 0);
-                tma_load_3d(sfb_buf + (size_t)i * SF_BYTES, &xsmap, &full[i], 0, (kb_lo + i) * SF_TILES, 0);
-            }
+            for (int i = 0; i < head; ++i) load_x(i, i);
         }
     }
     __syncwarp();
@@ -125,7 +135,7 @@ __global__ void __launch_bounds__(fp4f::THREADS)
     }
     if (FUSED) {
         // scale bytes past K are zero: what they multiply is, too, and must not meet a NaN
-        for (uint32_t i = tid; i < p.kb_per * SF_BYTES / 16; i += THREADS)
+        for (uint32_t i = tid; i < b_steps * SF_BYTES / 16; i += THREADS)
             reinterpret_cast<uint4*>(sfb_buf)[i] = make_uint4(0, 0, 0, 0);
     }
     tc_fence_before();
@@ -181,6 +191,21 @@ __global__ void __launch_bounds__(fp4f::THREADS)
         __syncthreads();
     }
 
+    if (RING && warp == 0) {
+        // ---------------------------------------------------------------- the steps that did not fit
+        if (elect_one()) {
+            if (!FUSED) grid_dependency_wait();   // its waits need the kernel before this one
+            int i = R;
+            for (; i < n_kb; ++i) {
+                const int slot = i % R;
+                if (!mbar_wait(&empty[slot], (uint32_t)(i / R - 1) & 1u, &abort_flag, p.dev_status)) break;
+                load_w(i, slot);
+                if (!FUSED) load_x(i, slot);
+            }
+            loaded = i;
+        }
+        __syncwarp();
+    }
     if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (elect_one()) {
@@ -189,19 +214,21 @@ __global__ void __launch_bounds__(fp4f::THREADS)
             const uint64_t fa = smem_desc_scales(smem_u32(sfa_buf)), fb = smem_desc_scales(smem_u32(sfb_buf));
             const uint32_t ab_hi = (uint32_t)(ad >> 32), sf_hi = (uint32_t)(fa >> 32);
             bool ok = true;
+            int slot = 0;
+            uint32_t phase = 0;
             for (int i = 0; i < n_kb; ++i) {
-                if (!mbar_wait(&full[i], 0, &abort_flag, p.dev_status)) {
+                if (!mbar_wait(&full[slot], phase, &abort_flag, p.dev_status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t a_lo = (uint32_t)ad + i * (A_BYTES >> 4), b_lo = (uint32_t)bd + i * (p.b_bytes >> 4);
+                const int b = FUSED ? i : slot;
+                const uint32_t a_lo = (uint32_t)ad + slot * (A_BYTES >> 4), b_lo = (uint32_t)bd + b * (p.b_bytes >> 4);
                 const uint32_t sfa = tmem_base + SF_COL + (i & 1) * 32, sfb = sfa + 16;
 #pragma unroll
                 for (int j = 0; j < SF_TILES; ++j) {
-                    const uint32_t off = (i * SF_BYTES + j * kFp4TileBytes) >> 4;
-                    tc_cp_scales<1>(sfa + 4 * j, (uint32_t)fa + off, sf_hi);
-                    tc_cp_scales<1>(sfb + 4 * j, (uint32_t)fb + off, sf_hi);
+                    tc_cp_scales<1>(sfa + 4 * j, (uint32_t)fa + ((slot * SF_BYTES + j * kFp4TileBytes) >> 4), sf_hi);
+                    tc_cp_scales<1>(sfb + 4 * j, (uint32_t)fb + ((b * SF_BYTES + j * kFp4TileBytes) >> 4), sf_hi);
                 }
                 const int steps = min(4, (int)((p.K - (int64_t)(kb_lo + i) * BK + 63) / 64));
 #pragma unroll
@@ -212,6 +239,11 @@ __global__ void __launch_bounds__(fp4f::THREADS)
                                           p.idesc | (half << 4) | (half << 29), sfa + 4 * tile, sfb + 4 * tile,
                                           (i | j) != 0 ? 1u : 0u);
                     }
+                }
+                if (RING) tc_commit(&empty[slot]);
+                if (++slot == R) {
+                    slot = 0;
+                    phase ^= 1u;
                 }
             }
             if (ok) tc_commit(&acc_full);
@@ -279,7 +311,8 @@ __global__ void __launch_bounds__(fp4f::THREADS)
     // no CTA leaves while a peer may still read its partial sums, nor with a copy still landing
     cluster_sync_all();
     if (tid == 0 && abort_flag)
-        for (int i = 0; i < n_kb; ++i) mbar_wait(&full[i], 0, nullptr, nullptr);
+        for (int i = max(loaded - R, 0); i < loaded; ++i)
+            mbar_wait(&full[i % R], (uint32_t)(i / R) & 1u, nullptr, nullptr);
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
@@ -287,32 +320,28 @@ __global__ void __launch_bounds__(fp4f::THREADS)
     }
 }
 
-// Shared memory of a CTA with kb_per steps and BN rows.
-static size_t few_smem_bytes(int kb_per, int bn) {
+// Shared memory of a CTA: `slots` steps of weights, `b_steps` steps of BN rows, the partial sums.
+static size_t few_smem_bytes(int slots, int b_steps, int bn, bool nv) {
     using namespace fp4f;
-    return 1024 + (size_t)kb_per * (A_BYTES + (size_t)bn * (BK / 2) + 2 * SF_BYTES) + (size_t)bn * BW * 4;
+    const size_t sf = (nv ? 4 : 2) * kFp4TileBytes;
+    return 1024 + slots * (A_BYTES + sf) + b_steps * ((size_t)bn * (BK / 2) + sf) + (size_t)bn * BW * 4;
 }
 
 static int few_bn(int64_t M) { return M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
-// The most steps a CTA holds.
-static int few_kb_max(int bn) {
-    int kb = fp4f::KB_MAX;
-    while (kb > 0 && few_smem_bytes(kb, bn) > fp4f::SMEM_BUDGET) --kb;
-    return kb;
+bool fp4_few_takes(int64_t M) { return M >= 1 && M <= 64; }
+
+// Rows x steps of 256 k up to which the tiles quantize for themselves.  Measured (3840 channels, replayed,
+// bf16): K = 3840, 8 rows: MX 6.9 us and NV 8.1 against 7.3 and 7.9 with the quantizer in a launch of its
+// own; 16 rows: 8.1 and 9.7 against 7.3 and 7.9; but that launch also costs the host 3 us.
+bool fp4_few_fuses(int64_t M, int64_t K) {
+    return fp4_few_takes(M) && M <= 16 && M * ((K + fp4f::BK - 1) / fp4f::BK) <= 180;
 }
 
-bool fp4_few_takes(int64_t M, int64_t K) {
-    if (M < 1 || M > 64) return false;
-    return (K + fp4f::BK - 1) / fp4f::BK <= (int64_t)fp4f::MAX_CLUSTER * few_kb_max(few_bn(M));
-}
-
-bool fp4_few_fuses(int64_t M, int64_t K) { return M <= 16 && fp4_few_takes(M, K); }
-
-template <typename T, bool NV, bool HAS_T, bool FUSED>
-static ck_status few_launch(const CUtensorMap* maps, const Fp4FewParams& p, int S, int tiles_n, size_t smem,
+template <typename T, bool NV, bool HAS_T, bool FUSED, bool RING>
+static ck_status few_launch_ring(const CUtensorMap* maps, const Fp4FewParams& p, int S, int tiles_n, size_t smem,
                             bool dep, cudaStream_t stream) {
-    auto kern = fp4_few_kernel<T, NV, HAS_T, FUSED>;
+    auto kern = fp4_few_kernel<T, NV, HAS_T, FUSED, RING>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return CK_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -331,6 +360,14 @@ static ck_status few_launch(const CUtensorMap* maps, const Fp4FewParams& p, int 
     cfg.numAttrs = dep ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p) != cudaSuccess) return CK_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? CK_OK : CK_ERR_CUDA;
+}
+
+template <typename T, bool NV, bool HAS_T, bool FUSED>
+static ck_status few_launch(const CUtensorMap* maps, const Fp4FewParams& p, int S, int tiles_n, size_t smem,
+                            bool dep, cudaStream_t stream) {
+    return p.kb_per > p.slots
+               ? few_launch_ring<T, NV, HAS_T, FUSED, true>(maps, p, S, tiles_n, smem, dep, stream)
+               : few_launch_ring<T, NV, HAS_T, FUSED, false>(maps, p, S, tiles_n, smem, dep, stream);
 }
 
 template <typename T>
@@ -354,16 +391,20 @@ ck_status launch_fp4_few(const Fp4Product& a, const void* x, ck_dtype x_dt, int6
     p.num_kb = (int)((a.K + BK - 1) / BK);
     const int64_t tiles_n = (a.N + BW - 1) / BW;
     if (tiles_n >= 65536) return CK_ERR_UNSUPPORTED;
-    // the smallest split that gives three SMs in four a CTA (3840 x 3840, 32 rows: 4 CTAs a tile 7.45 us,
-    // 3 and 5: 8.1 and 7.7), and no more steps than a CTA holds
-    const int kb_max = few_kb_max(p.BN), sms = num_sms();
+    // The smallest split that gives three SMs in four a CTA (3840 x 3840, 32 rows: 4 CTAs a tile 7.45 us,
+    // 3 and 5: 8.1 and 7.7), and, fused, leaves half of shared memory for weights.
+    const int sms = num_sms();
     int S = 1;
-    while (S < MAX_CLUSTER && 4 * S * tiles_n < 3 * (int64_t)sms) ++S;
-    const int least = (p.num_kb + kb_max - 1) / kb_max;
-    if (S < least) S = least;
-    if (S > p.num_kb) S = p.num_kb;
-    p.kb_per = (p.num_kb + S - 1) / S;
+    for (;; ++S) {
+        p.kb_per = (p.num_kb + S - 1) / S;
+        const bool fits = !fused || few_smem_bytes(0, p.kb_per, p.BN, a.nv) <= SMEM_BUDGET / 2;
+        if ((4 * S * tiles_n >= 3 * (int64_t)sms && fits) || S == MAX_CLUSTER || S >= p.num_kb) break;
+    }
     S = (p.num_kb + p.kb_per - 1) / p.kb_per;   // every rank has a step
+    p.slots = p.kb_per < SLOTS_MAX ? p.kb_per : SLOTS_MAX;
+    while (p.slots > 1 && few_smem_bytes(p.slots, fused ? p.kb_per : p.slots, p.BN, a.nv) > SMEM_BUDGET) --p.slots;
+    const size_t smem = few_smem_bytes(p.slots, fused ? p.kb_per : p.slots, p.BN, a.nv);
+    if (smem > SMEM_BUDGET) return CK_ERR_UNSUPPORTED;
     p.b_bytes = (uint32_t)p.BN * (BK / 2);
     p.idesc = idesc_fp4(BW, p.BN, a.nv);
     p.x = x;
@@ -414,7 +455,6 @@ ck_status launch_fp4_few(const Fp4Product& a, const void* x, ck_dtype x_dt, int6
                         CU_TENSOR_MAP_SWIZZLE_NONE);
         if (st != CK_OK) return st;
     }
-    const size_t smem = few_smem_bytes(p.kb_per, p.BN);
     if (!fused)
         return a.nv ? few_launch<float, true, false, false>(maps, p, S, (int)tiles_n, smem, a.dependent, stream)
                     : few_launch<float, false, false, false>(maps, p, S, (int)tiles_n, smem, a.dependent, stream);

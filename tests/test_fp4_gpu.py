@@ -339,7 +339,7 @@ def _close(got, exact, mag, K, what=""):
 
 
 SHAPES = [(1, 1, 32), (3, 5, 16), (70, 9, 16), (1, 3840, 3840), (7, 200, 16384), (8, 96, 272), (9, 4000, 1040), (15, 333, 10240), (16, 129, 16400),
-          (17, 130, 12320), (40, 200, 12304), (2, 40, 64), (5, 300, 96), (16, 130, 800), (31, 257, 1056),
+          (17, 130, 12320), (40, 200, 12304), (1, 300, 46080), (2, 260, 23040), (16, 150, 2816), (64, 300, 40000), (2, 40, 64), (5, 300, 96), (16, 130, 800), (31, 257, 1056),
           (33, 640, 2080), (64, 128, 256), (65, 129, 288), (100, 1111, 2064), (127, 500, 512),
           (128, 256, 4096), (200, 384, 1024), (413, 1111, 2064), (700, 1920, 544), (1500, 2049, 1040),
           (2500, 3840, 320), (4097, 1300, 272)]
@@ -771,6 +771,7 @@ def test_a_mixture_of_experts_layer(fmt):
 @FMT
 @pytest.mark.parametrize("what,M,N,K,E", [("few rows, from activations", 8, 512, 1024, 0),
                                           ("few rows, from codes", 40, 512, 1024, 0),
+                                          ("few rows, many steps", 40, 512, 30720, 0),
                                           ("one CTA a tile", 200, 256, 1024, 0),
                                           ("two CTAs a tile", 3000, 2048, 1024, 0),
                                           ("by expert", 300, 512, 1024, 4)])

@@ -338,7 +338,7 @@ ck_status ck_dequant_fp4(const uint8_t* codes, int64_t ldq, const uint8_t* scale
  *             values (at most 16 rows, M * ceil(K / 256) <= 180) are quantized inside the product's
  *             kernel.
  * Errors: CK_ERR_INVALID_ARG, CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED (a size of 2^31 or more, or as
- * many tiles; more than 8,388,480 channels with at most 64 rows), CK_ERR_CUDA.
+ * many tiles; more than 8,388,480 channels where x is quantized inside), CK_ERR_CUDA.
  */
 ck_status ck_fp4_linear(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, int64_t stride_m,
                         int64_t stride_k, ck_fp4_format format, const uint8_t* x_scales,

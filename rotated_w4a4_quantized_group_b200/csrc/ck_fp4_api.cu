@@ -65,14 +65,15 @@ static ck_status product(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, 
     a.out_dt = out_dtype;
     a.ldo = ldo;
     a.dev_status = dev_status;
-    const bool few = !offsets && fp4_few_takes(M);
+    const bool ragged = out_dtype != CK_F32 && (ldo % 8 != 0 || !aligned(out, 16));
+    const bool few = !offsets && fp4_few_takes(M, N, K, a.nv, ragged);
     if (codes_in) {
         a.codes = static_cast<const uint8_t*>(x);
         a.ldq = stride_m;
         a.scales = x_scales;
         return few ? launch_fp4_few(a, nullptr, x_dtype, 0, 0, stream) : launch_fp4_gemm(a, stream);
     }
-    if (few && fp4_few_fuses(M, K)) return launch_fp4_few(a, x, x_dtype, stride_m, stride_k, stream);
+    if (!offsets && fp4_few_fuses(M, K)) return launch_fp4_few(a, x, x_dtype, stride_m, stride_k, stream);
     const size_t need = ck_fp4_linear_workspace_bytes(M, K, format, offsets ? n_experts : 0);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return CK_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);

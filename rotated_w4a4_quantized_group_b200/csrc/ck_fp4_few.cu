@@ -1,10 +1,10 @@
-// ck_fp4_few.cu -- the fp4 linear for few rows (M <= 64): a read of the weights, and for the
-// smallest calls a chain of latencies.
+// ck_fp4_few.cu -- the fp4 linear for few rows or few tiles: a read of the weights, and for the smallest
+// calls a chain of latencies.
 //
 //   out[m, n] = cvt(fl(acc[m, n] * alpha) + bias[n]),   alpha = x_tensor_scale * w_tensor_scale
 //
-// 128-channel tiles alone would be N / 128 CTAs, so each tile's K is split over a cluster of S CTAs
-// (S * N / 128 about one per SM), each of which
+// Tiles of 128 channels x up to 64 rows alone would be a CTA on a few SMs, so each tile's K is split over
+// a cluster of S CTAs (about one per SM in all), each of which
 //   - asks for its share of the weights, as many steps of 256 k at once as shared memory holds (one
 //     box of codes and one of scale tiles a step, on the step's mbarrier), for the others as MMAs
 //     free their slots,
@@ -15,9 +15,9 @@
 //   - multiplies on the tensor cores, 128 channels x BN rows, as the weights arrive,
 //   - writes its partial sums to shared memory; after a cluster barrier each CTA adds its share of
 //     the tile over the S partials in rank order (no atomics) and stores it.
-// Measured, 3840 x 3840: one bf16 row to NV 7.0 us replayed back to back (10.2 with the quantizer and
-// the persistent kernel), 32 rows with the quantizer before it 7.5 (10.1); the weights alone are 1.3 us
-// of HBM.
+// Measured, 3840 x 3840: one bf16 row to NV 7.2 us replayed back to back (10.2 with the quantizer and
+// the persistent kernel), 32 rows to MX with the quantizer before it 7.6 (10.1); the weights alone are
+// 1.3 us of HBM.
 // Every CTA takes both cluster barriers whatever happened before them; every mbarrier wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -45,7 +45,7 @@ constexpr size_t SMEM_BUDGET = 220 * 1024;
 }  // namespace fp4f
 
 struct Fp4FewParams {
-    int M, BN;               // rows, and the MMA's N
+    int M, BN;               // rows, and rows of a tile: the MMA's N
     int64_t N, K;
     int num_kb, kb_per;      // steps of K, and of one CTA
     int slots;               // steps of weights (FUSED), or of both operands, held at a time
@@ -61,14 +61,9 @@ struct Fp4FewParams {
     void* out;
     ck_dtype out_dt;
     int64_t ldo;
+    bool out_vec;            // four outputs in one aligned store
     int* dev_status;
 };
-
-__device__ __forceinline__ float few_load(const void* p, ck_dtype dt, int64_t i) {
-    if (dt == CK_F32) return load_scale<float>(p, i);
-    if (dt == CK_F16) return load_scale<__half>(p, i);
-    return load_scale<__nv_bfloat16>(p, i);
-}
 
 // T: the activations' type (FUSED), otherwise ignored.  RING: a CTA has more steps than slots (the short
 // form saves the smallest calls half a microsecond of 6.5).
@@ -98,6 +93,8 @@ __global__ void __launch_bounds__(fp4f::THREADS)
     const int kb_lo = (int)rank * p.kb_per;
     const int n_kb = min(p.num_kb - kb_lo, p.kb_per);
     const int n0 = (int)blockIdx.y * BW;
+    const int m0 = FUSED ? 0 : (int)blockIdx.z * p.BN;      // the tile's first row, and its rows
+    const int rows = min(p.M - m0, p.BN);
 
     auto load_w = [&](int i, int slot) {
         mbar_arrive_expect_tx(&full[slot], A_BYTES + SF_BYTES);
@@ -107,8 +104,9 @@ __global__ void __launch_bounds__(fp4f::THREADS)
     };
     auto load_x = [&](int i, int slot) {
         mbar_arrive_expect_tx(&full[slot], p.b_bytes + SF_BYTES);
-        tma_load_2d(bbuf + (size_t)slot * p.b_bytes, &xmap, &full[slot], (kb_lo + i) * (BK / 2), 0);
-        tma_load_3d(sfb_buf + (size_t)slot * SF_BYTES, &xsmap, &full[slot], 0, (kb_lo + i) * SF_TILES, 0);
+        tma_load_2d(bbuf + (size_t)slot * p.b_bytes, &xmap, &full[slot], (kb_lo + i) * (BK / 2), m0);
+        tma_load_3d(sfb_buf + (size_t)slot * SF_BYTES, &xsmap, &full[slot], 0, (kb_lo + i) * SF_TILES,
+                    m0 / kFp4TileRows);
     };
     const int head = RING ? min(n_kb, R) : n_kb;   // steps asked for at once
     if (tid == 0) {
@@ -148,7 +146,7 @@ __global__ void __launch_bounds__(fp4f::THREADS)
         const int64_t k0 = (int64_t)kb_lo * BK;
         const int64_t left = p.K - k0;
         const int groups = (int)min(left, (int64_t)n_kb * BK) / 16;   // of sixteen k; even for MX
-        const int total = p.M * groups;
+        const int total = rows * groups;
         Fp4Tensor t = fp4_tensor(HAS_T ? p.x_ts : nullptr);
         if (HAS_T && GridBits<T>::value > 0) t.moves = fp4_moves<T>(t.t);
         const T* x = static_cast<const T*>(p.x);
@@ -214,6 +212,7 @@ __global__ void __launch_bounds__(fp4f::THREADS)
             const uint64_t fa = smem_desc_scales(smem_u32(sfa_buf)), fb = smem_desc_scales(smem_u32(sfb_buf));
             const uint32_t ab_hi = (uint32_t)(ad >> 32), sf_hi = (uint32_t)(fa >> 32);
             bool ok = true;
+            const uint32_t shift = (uint32_t)(m0 % kFp4TileRows) / 32;   // the rows' first scale column
             int slot = 0;
             uint32_t phase = 0;
             for (int i = 0; i < n_kb; ++i) {
@@ -236,8 +235,8 @@ __global__ void __launch_bounds__(fp4f::THREADS)
                     if (j < steps) {
                         const uint32_t tile = NV ? j : j >> 1, half = NV ? 0u : (j & 1u) * 2u;
                         tc_mma_fp4<NV, 1>(tmem_base, a_lo + j * 2, b_lo + j * 2, ab_hi,
-                                          p.idesc | (half << 4) | (half << 29), sfa + 4 * tile, sfb + 4 * tile,
-                                          (i | j) != 0 ? 1u : 0u);
+                                          p.idesc | (half << 4) | (half << 29), sfa + 4 * tile,
+                                          sfb + 4 * tile + shift, (i | j) != 0 ? 1u : 0u);
                     }
                 }
                 if (RING) tc_commit(&empty[slot]);
@@ -260,13 +259,13 @@ __global__ void __launch_bounds__(fp4f::THREADS)
         if (__all_sync(0xffffffffu, mbar_wait(&acc_full, 0, &abort_flag, p.dev_status))) {
             tc_fence_after();
             const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
-            for (int m0 = 0; m0 < p.M; m0 += 16) {
+            for (int c = 0; c < rows; c += 16) {
                 uint32_t a[16];
-                tc_ld_32x32b_x16(tacc + (uint32_t)m0, a);
+                tc_ld_32x32b_x16(tacc + (uint32_t)c, a);
                 tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (m0 + j < p.M) partial[(m0 + j) * BW + q * 32 + lane] = __uint_as_float(a[j]);
+                    if (c + j < rows) partial[(c + j) * BW + q * 32 + lane] = __uint_as_float(a[j]);
             }
         }
         tc_fence_before();
@@ -278,7 +277,7 @@ __global__ void __launch_bounds__(fp4f::THREADS)
     if (!FUSED) grid_dependency_wait();   // also what this kernel writes waits for the one before
     if (!abort_flag) {
         const float alpha = __fmul_rn(p.x_ts ? __ldg(p.x_ts) : 1.0f, p.w_ts ? __ldg(p.w_ts) : 1.0f);
-        const int nvec = p.M * (BW / 4);
+        const int nvec = rows * (BW / 4);
         const int lo = (int)((int64_t)nvec * rank / ncta), hi = (int)((int64_t)nvec * (rank + 1) / ncta);
         for (int vi = lo + tid; vi < hi; vi += THREADS) {
             const int m = vi / (BW / 4), c4 = (vi % (BW / 4)) * 4;
@@ -295,16 +294,30 @@ __global__ void __launch_bounds__(fp4f::THREADS)
                     s[2] = __fadd_rn(s[2], __uint_as_float(u[q].z));
                     s[3] = __fadd_rn(s[3], __uint_as_float(u[q].w));
                 }
+            const int64_t n = (int64_t)n0 + c4, at = (int64_t)(m0 + m) * p.ldo + n;
+            const int have = (int)min(p.N - n, (int64_t)4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int64_t n = (int64_t)n0 + c4 + e;
-                if (n >= p.N) break;
-                float o = __fmul_rn(s[e], alpha);
-                if (p.bias) o = __fadd_rn(o, few_load(p.bias, p.bias_dt, n));
-                const int64_t at = m * p.ldo + n;
-                if (p.out_dt == CK_F32) static_cast<float*>(p.out)[at] = o;
-                else if (p.out_dt == CK_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(o);
-                else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
+                s[e] = __fmul_rn(s[e], alpha);
+                if (p.bias && e < have) s[e] = __fadd_rn(s[e], load_any(p.bias, p.bias_dt, n + e));
+            }
+            if (p.out_vec && have == 4) {   // four channels in one store
+                if (p.out_dt == CK_F32) {
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(s[0], s[1], s[2], s[3]);
+                } else {
+                    const uint2 u = p.out_dt == CK_F16 ? make_uint2(pack2<__half>(s[0], s[1]), pack2<__half>(s[2], s[3]))
+                                                       : make_uint2(pack2<__nv_bfloat16>(s[0], s[1]),
+                                                                    pack2<__nv_bfloat16>(s[2], s[3]));
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = u;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (e >= have) break;
+                    if (p.out_dt == CK_F32) static_cast<float*>(p.out)[at + e] = s[e];
+                    else if (p.out_dt == CK_F16) static_cast<__half*>(p.out)[at + e] = __float2half_rn(s[e]);
+                    else static_cast<__nv_bfloat16*>(p.out)[at + e] = __float2bfloat16_rn(s[e]);
+                }
             }
         }
     }
@@ -329,13 +342,61 @@ static size_t few_smem_bytes(int slots, int b_steps, int bn, bool nv) {
 
 static int few_bn(int64_t M) { return M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
-bool fp4_few_takes(int64_t M) { return M >= 1 && M <= 64; }
+// How a call is split: S CTAs a tile, kb_per steps a CTA, `slots` of them in flight, shared memory.
+struct FewPlan {
+    int S, kb_per, slots;
+    size_t smem;
+};
+
+// The largest split whose clusters all run at once: a second round costs more than any split gains (16
+// tiles of 10240 k in clusters of eight took 13 us, 12 tiles 7.8).  The room is what a B200 holds of
+// clusters of S (they do not cross GPCs) with one CTA an SM and with two, where shared memory fits twice.
+static FewPlan few_plan(int64_t tiles, int64_t num_kb, int bn, bool nv, bool fused) {
+    using namespace fp4f;
+    static const struct {
+        int S, room[2];
+    } splits[] = {{8, {15, 33}}, {6, {22, 45}}, {5, {26, 56}}, {4, {33, 71}}, {3, {45, 93}}, {2, {74, 148}}, {1, {148, 296}}};
+    FewPlan r = {};
+    for (const auto& c : splits) {
+        FewPlan p;
+        p.kb_per = (int)((num_kb + c.S - 1) / c.S);
+        p.S = (int)((num_kb + p.kb_per - 1) / p.kb_per);   // every rank has a step
+        // fused, half of shared memory stays for weights: otherwise the larger split, in several rounds
+        if (fused && r.S && few_smem_bytes(0, p.kb_per, bn, nv) > SMEM_BUDGET / 2) break;
+        p.slots = p.kb_per < SLOTS_MAX ? p.kb_per : SLOTS_MAX;
+        while (p.slots > 1 && few_smem_bytes(p.slots, fused ? p.kb_per : p.slots, bn, nv) > SMEM_BUDGET) --p.slots;
+        p.smem = few_smem_bytes(p.slots, fused ? p.kb_per : p.slots, bn, nv);
+        r = p;
+        // (large clusters of more than 16 rows lose that way: 64 rows of 3840x3840 in sixes 9.2 us, in fours 8.85)
+        const bool twice = 2 * (p.smem + 2048) <= 228 * 1024 && (c.S <= 4 || bn <= 16);
+        if (tiles <= c.room[twice]) break;
+    }
+    return r;
+}
+
+static int64_t few_tiles(int64_t M, int64_t N) {
+    const int bn = few_bn(M);
+    return ((N + fp4f::BW - 1) / fp4f::BW) * ((M + bn - 1) / bn);
+}
+
+// From codes: whether the split takes less than the persistent kernel.  Both measured on 17 to 600 rows,
+// 64 to 3840 channels and 256 to 10240 k, us: the split 4.3, 0.02 a row of the tile, 0.5 a further step
+// and 1.1 where CTAs share SMs; the persistent kernel, while its tiles are one round, 3.9, 0.26 a step,
+// and 1.1 where 16-bit rows do not take 16-byte stores (`ragged`).  100 x 907 x 10240: 8.8 against 15.1.
+bool fp4_few_takes(int64_t M, int64_t N, int64_t K, bool nv, bool ragged) {
+    const int64_t tiles = few_tiles(M, N), num_kb = (K + fp4f::BK - 1) / fp4f::BK;
+    if (M < 1 || 2 * tiles > num_sms()) return false;
+    const int bn = few_bn(M);
+    const FewPlan r = few_plan(tiles, num_kb, bn, nv, false);
+    const double shared = tiles * r.S > num_sms() ? 1.1 : 0.0;
+    return 4.3 + 0.02 * bn + 0.5 * (r.kb_per - 1) + shared < 3.9 + 0.26 * (double)num_kb + (ragged ? 1.1 : 0.0);
+}
 
 // Rows x steps of 256 k up to which the tiles quantize for themselves.  Measured (3840 channels, replayed,
 // bf16): K = 3840, 8 rows: MX 6.9 us and NV 8.1 against 7.3 and 7.9 with the quantizer in a launch of its
 // own; 16 rows: 8.1 and 9.7 against 7.3 and 7.9; but that launch also costs the host 3 us.
 bool fp4_few_fuses(int64_t M, int64_t K) {
-    return fp4_few_takes(M) && M <= 16 && M * ((K + fp4f::BK - 1) / fp4f::BK) <= 180;
+    return M >= 1 && M <= 16 && M * ((K + fp4f::BK - 1) / fp4f::BK) <= 180;
 }
 
 template <typename T, bool NV, bool HAS_T, bool FUSED, bool RING>
@@ -352,7 +413,7 @@ static ck_status few_launch_ring(const CUtensorMap* maps, const Fp4FewParams& p,
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_n, 1);
+    cfg.gridDim = dim3((unsigned)S, (unsigned)tiles_n, (unsigned)((p.M + p.BN - 1) / p.BN));
     cfg.blockDim = dim3(fp4f::THREADS, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -389,22 +450,14 @@ ck_status launch_fp4_few(const Fp4Product& a, const void* x, ck_dtype x_dt, int6
     p.N = a.N;
     p.K = a.K;
     p.num_kb = (int)((a.K + BK - 1) / BK);
-    const int64_t tiles_n = (a.N + BW - 1) / BW;
-    if (tiles_n >= 65536) return CK_ERR_UNSUPPORTED;
-    // The smallest split that gives three SMs in four a CTA (3840 x 3840, 32 rows: 4 CTAs a tile 7.45 us,
-    // 3 and 5: 8.1 and 7.7), and, fused, leaves half of shared memory for weights.
-    const int sms = num_sms();
-    int S = 1;
-    for (;; ++S) {
-        p.kb_per = (p.num_kb + S - 1) / S;
-        const bool fits = !fused || few_smem_bytes(0, p.kb_per, p.BN, a.nv) <= SMEM_BUDGET / 2;
-        if ((4 * S * tiles_n >= 3 * (int64_t)sms && fits) || S == MAX_CLUSTER || S >= p.num_kb) break;
-    }
-    S = (p.num_kb + p.kb_per - 1) / p.kb_per;   // every rank has a step
-    p.slots = p.kb_per < SLOTS_MAX ? p.kb_per : SLOTS_MAX;
-    while (p.slots > 1 && few_smem_bytes(p.slots, fused ? p.kb_per : p.slots, p.BN, a.nv) > SMEM_BUDGET) --p.slots;
-    const size_t smem = few_smem_bytes(p.slots, fused ? p.kb_per : p.slots, p.BN, a.nv);
+    const int64_t tiles_n = (a.N + BW - 1) / BW, tiles_m = (a.M + p.BN - 1) / p.BN;
+    if (tiles_n >= 65536 || tiles_m >= 65536) return CK_ERR_UNSUPPORTED;
+    const FewPlan plan = few_plan(tiles_n * tiles_m, p.num_kb, p.BN, a.nv, fused);
+    const int S = plan.S;
+    const size_t smem = plan.smem;
     if (smem > SMEM_BUDGET) return CK_ERR_UNSUPPORTED;
+    p.kb_per = plan.kb_per;
+    p.slots = plan.slots;
     p.b_bytes = (uint32_t)p.BN * (BK / 2);
     p.idesc = idesc_fp4(BW, p.BN, a.nv);
     p.x = x;
@@ -419,6 +472,7 @@ ck_status launch_fp4_few(const Fp4Product& a, const void* x, ck_dtype x_dt, int6
     p.out = a.out;
     p.out_dt = a.out_dt;
     p.ldo = a.ldo;
+    p.out_vec = a.ldo % 4 == 0 && aligned(a.out, a.out_dt == CK_F32 ? 16 : 8);
     p.dev_status = a.dev_status;
 
     CUtensorMap maps[4];
@@ -448,7 +502,7 @@ ck_status launch_fp4_few(const Fp4Product& a, const void* x, ck_dtype x_dt, int6
         ck_status st = encode_tma(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.codes, dims, strides, box,
                                   CU_TENSOR_MAP_SWIZZLE_128B);
         if (st != CK_OK) return st;
-        const uint64_t sdims[3] = {words, k_tiles, 1};
+        const uint64_t sdims[3] = {words, k_tiles, (uint64_t)((a.M + kFp4TileRows - 1) / kFp4TileRows)};
         const uint64_t sstrides[2] = {kFp4TileBytes, k_tiles * kFp4TileBytes};
         const uint32_t sbox[3] = {(uint32_t)words, sf_tiles, 1};
         st = encode_tma(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, a.scales, sdims, sstrides, sbox,

@@ -52,18 +52,6 @@ constexpr size_t SMEM_MAX = 227 * 1024 - 1024;   // less the static shared memor
 static_assert(SF_COL + 2 * SF_SET <= TMEM_COLS, "accumulators and scales fit");
 }  // namespace fp4g
 
-template <typename OutT> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    return 0u;   // fp32 outputs are not packed
-}
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 struct Fp4GemmParams {
     int64_t M, N;
     int num_kb;           // stages per tile: ceil(K / 256)
@@ -85,12 +73,6 @@ struct Fp4GemmParams {
     int64_t ldo;
     int* dev_status;
 };
-
-__device__ __forceinline__ float load_any(const void* p, ck_dtype dt, int64_t i) {
-    if (dt == CK_F32) return load_scale<float>(p, i);
-    if (dt == CK_F16) return load_scale<__half>(p, i);
-    return load_scale<__nv_bfloat16>(p, i);
-}
 
 // One tile: expert, first row, rows, first channel of the CTA's 128, and where its rows' scales are.
 struct Fp4Tile {

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "ck_device.cuh"
+#include "ck_gemm_common.cuh"
 
 namespace ck {
 
@@ -255,6 +256,28 @@ __device__ __forceinline__ void tc_mma_fp4(uint32_t d_tmem, uint32_t a_lo, uint3
         else CK_FP4_MMA("2", "2X");
     }
 #undef CK_FP4_MMA
+}
+
+// ------------------------------------------------------------------ outputs
+
+// Two outputs of a 16-bit type in one word, the first in its low half.
+template <typename OutT> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return 0u;   // fp32 outputs are not packed
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A bias of any of the three types.
+__device__ __forceinline__ float load_any(const void* p, ck_dtype dt, int64_t i) {
+    if (dt == CK_F32) return load_scale<float>(p, i);
+    if (dt == CK_F16) return load_scale<__half>(p, i);
+    return load_scale<__nv_bfloat16>(p, i);
 }
 
 }  // namespace ck

@@ -155,9 +155,9 @@ struct Fp4Product {
     int* dev_status;
 };
 ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream);   // ck_fp4_gemm.cu
-// Few rows of one matrix (ck_fp4_few.cu), where fp4_few_takes: from codes, or, where fp4_few_fuses and
-// a.codes is NULL, from the activations x, quantized on the way.
-bool fp4_few_takes(int64_t M);
+// Few rows or few tiles of one matrix (ck_fp4_few.cu), where fp4_few_takes: from codes, or, where
+// fp4_few_fuses and a.codes is NULL, from the activations x, quantized on the way.
+bool fp4_few_takes(int64_t M, int64_t N, int64_t K, bool nv, bool ragged);
 bool fp4_few_fuses(int64_t M, int64_t K);
 ck_status launch_fp4_few(const Fp4Product& a, const void* x, ck_dtype x_dt, int64_t sm, int64_t sk,
                          cudaStream_t stream);

@@ -368,6 +368,32 @@ def test_linear(fmt, M, N, K):
 
 
 @FMT
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(65, 64, 3840), (100, 907, 10240), (128, 640, 2048), (191, 130, 16640),
+                                   (257, 300, 46080), (300, 1111, 4128), (640, 388, 2848), (1000, 60, 5120)])
+def test_linear_of_few_tiles(fmt, dt, M, N, K):
+    """K split over several CTAs a tile, with tiles of rows that end inside a tile of scales: activations
+    and codes in, an output with a pitch, and the rows and columns around it left alone."""
+    x = _x(M, K, dt, 15, spread=False)
+    w, ws, wv = _weights(1, N, K, fmt, 16)
+    bias = (torch.randn(N, generator=_gen(17)) * 0.3).to(dt).cuda()
+    codes, scales = ck.ck_quant_fp4(x.cuda(), fmt)
+    xv = _xvalues(x, fmt, None)
+    exact, mag = xv @ wv[0].t() + bias.double(), xv.abs() @ wv[0].abs().t() + bias.double().abs()
+    for pad, first in ((8, 0), (5, 1)):
+        buf = torch.full((M + 2, N + pad), 7.25, dtype=dt, device="cuda")
+        out = buf[1:1 + M, first:first + N]
+        ck.ck_fp4_linear(codes, w[0], ws[0], fmt, bias, x_scales=scales, out=out)
+        _close(out, exact, mag, K, f"pad {pad}")
+        buf[1:1 + M, first:first + N] = 7.25
+        assert (buf == 7.25).all()
+    buf = torch.empty(M, N, dtype=dt, device="cuda")
+    again = ck.ck_fp4_linear(x.cuda(), w[0], ws[0], fmt, bias, out=buf)
+    assert torch.equal(again, ck.ck_fp4_linear(x.cuda(), w[0], ws[0], fmt, bias))
+    _close(again, exact, mag, K, "activations")
+
+
+@FMT
 @pytest.mark.parametrize("M,N,K", [(7, 130, 512), (70, 300, 1024), (300, 900, 768), (3000, 2000, 512)])
 def test_product_of_small_integers_is_exact(fmt, M, N, K):
     """Unit scales and codes: every partial sum is a multiple of 1/4 below 36 K, exact in fp32."""

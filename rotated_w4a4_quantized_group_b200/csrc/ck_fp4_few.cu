@@ -273,6 +273,12 @@ __global__ void __launch_bounds__(fp4f::THREADS)
 
     // ---------------------------------------------------------------- sum over the cluster
     __syncthreads();
+    if (warp == 1) {
+        // before the cluster's barrier: a CTA that held tensor memory there could wait for a peer that
+        // waits for tensor memory of its own, which such a CTA of another cluster holds
+        tc_fence_after();
+        tmem_dealloc(tmem_base, TMEM_COLS);
+    }
     cluster_sync_all();
     if (!FUSED) grid_dependency_wait();   // also what this kernel writes waits for the one before
     if (!abort_flag) {
@@ -326,11 +332,6 @@ __global__ void __launch_bounds__(fp4f::THREADS)
     if (tid == 0 && abort_flag)
         for (int i = max(loaded - R, 0); i < loaded; ++i)
             mbar_wait(&full[i % R], (uint32_t)(i / R) & 1u, nullptr, nullptr);
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem_base, TMEM_COLS);
-    }
 }
 
 // Shared memory of a CTA: `slots` steps of weights, `b_steps` steps of BN rows, the partial sums.

@@ -598,6 +598,10 @@ def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_sc
     _check_fp4(fmt, K)
     dev = _on_device(x, w, w_scales, bias, x_tensor_scale, w_tensor_scale, offsets, out, x_scales,
                      workspace, dev_status)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous; got strides {workspace.stride()}")
+    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.numel() < 1):
+        raise ValueError(f"dev_status must be an int32 tensor; got {dev_status.numel()} of {dev_status.dtype}")
     half = K // 2
     nE = 0 if offsets is None else E
     w_strides = w.stride()

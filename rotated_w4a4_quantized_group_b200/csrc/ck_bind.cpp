@@ -57,7 +57,8 @@ int float_code(at::ScalarType s) {
 }
 
 bool format_of(PyObject* o, ck_fp4_format& f) {
-    const long v = PyLong_Check(o) ? PyLong_AsLong(o) : -1;
+    int beyond;
+    const long v = PyLong_Check(o) ? PyLong_AsLongAndOverflow(o, &beyond) : -1;
     if (v != CK_MXFP4 && v != CK_NVFP4) return false;
     f = static_cast<ck_fp4_format>(v);
     return true;
@@ -159,6 +160,8 @@ PyObject* py_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
                   wts = optional(a[8], dev, ok), given = optional(a[9], dev, ok), work = optional(a[11], dev, ok),
                   dst = optional(a[12], dev, ok);
         const int64_t E = experts(off);
+        if ((work.t && !work.t->is_contiguous()) || (dst.t && (dst.t->scalar_type() != at::kInt || dst.t->numel() < 1)))
+            return none();
         if (!ok || E < 0 || !w.t || !wsc.t || w.t->dim() != (E ? 3 : 2)) return none();
         const bool codes_in = x->scalar_type() == at::kByte;
         const int dt = codes_in ? (int)CK_FP4 : float_code(x->scalar_type());

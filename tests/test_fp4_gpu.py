@@ -673,6 +673,51 @@ def test_two_calls_at_once_on_two_streams(fmt, M):
         assert all(torch.equal(o, b) for o in a)
 
 
+def test_many_calls_at_once():
+    """Calls on eight streams, pairs, clusters and single CTAs among them, more than the GPU holds at a
+    time: none waits for tensor memory that a call waiting for it holds."""
+    cases = [_case(NV if i % 2 else MX, M, N, K, seed=60 + i) + (NV if i % 2 else MX,)
+             for i, (M, N, K) in enumerate([(2, 3840, 512), (8, 3840, 1024), (40, 3840, 2048), (100, 907, 4096),
+                                            (600, 2048, 512), (1, 7680, 768), (33, 2048, 2816), (12, 3840, 2304)])]
+    want = [ck.ck_fp4_linear(x, w, ws, fmt) for x, w, ws, fmt in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(40):
+        for i, (x, w, ws, fmt) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(ck.ck_fp4_linear(x, w, ws, fmt))
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        assert all(torch.equal(o, want[i]) for o in outs), f"case {i}"
+
+
+@FMT
+@DT
+@pytest.mark.parametrize("M", [7, 40])
+def test_broadcast_and_overlapping_activations(fmt, dt, M):
+    _, w, ws = _case(fmt, 1, 130, 544)
+    row, col = _x(1, 544, dt, 65).cuda(), _x(M, 1, dt, 66).cuda()
+    flat = _x(1, 544 + 3 * M, dt, 67).cuda()[0]
+    for x in (row.expand(M, 544), col.expand(M, 544), flat.as_strided((M, 544), (1, 1)),
+              flat.as_strided((M, 544), (3, 1))):
+        for a, b in zip(ck.ck_quant_fp4(x, fmt), ck.ck_quant_fp4(x.contiguous(), fmt)):
+            assert torch.equal(a, b)
+        assert torch.equal(ck.ck_fp4_linear(x, w, ws, fmt), ck.ck_fp4_linear(x.contiguous(), w, ws, fmt))
+
+
+def test_what_a_call_would_write_past_is_refused():
+    x, w, ws = _case(NV, 40, 64, 512)
+    for kw in ({"dev_status": torch.zeros(4, dtype=torch.uint8, device="cuda")},
+               {"dev_status": torch.zeros(0, dtype=torch.int32, device="cuda")},
+               {"workspace": torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 20)}):
+        with pytest.raises(ValueError):
+            ck.ck_fp4_linear(x, w, ws, NV, **kw)
+    for fmt in (2, -1, 2 ** 70, None, "NV"):
+        with pytest.raises(ValueError):
+            ck.ck_fp4_linear(x, w, ws, fmt)
+
+
 def test_callers_workspace_and_its_layout():
     M, N, K = 100, 200, 544
     x, w, ws = _case(NV, M, N, K)

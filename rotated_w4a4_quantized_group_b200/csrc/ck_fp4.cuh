@@ -151,20 +151,23 @@ struct Fp4Tensor {
     bool t_ok;    // a positive finite number; otherwise every scale is NaN
     bool t_mid;   // far enough from the ends for every s t and its reciprocal to be normal
     // bits 4 i to 4 i + 3, signed: how many steps the reciprocal of blocks whose scale has mantissa
-    // 1 + i / 8 is moved; 1 where they take the rounded quotient instead
+    // 1 + i / 8 is moved; -8 where some borders want -8 and others 8
     uint32_t moves;
+    uint32_t ups;   // bit 4 i + j: that scale's borders of mantissa 1 + j / 4 want the larger one
 };
 
 // x * r, r within a step of 1 / d, d = fl(s t), rounds to the code of x / d for every x of a 16-bit
 // type but those on which a border (0.25 to 5; four mantissas) times d all but falls: with t an
-// absmax / 2688, the usual calibration, every third block has such a border.  They want r a little
-// larger (x above its border), a little smaller (below), or exact; which depends on the mantissas of
-// s, border and t alone, so a warp finds it once for all 8 x 4 pairs.  In steps of a mantissa: r, the
-// product and the border are off by less than 3 together, so seven decide every such x, and no value
+// absmax / 2688, the usual calibration, every third block has such a border, and with a t of few bits
+// x may be on it.  They want r a little larger (x above its border, or to be rounded up from it) or a
+// little smaller, which depends on the mantissas of s, border and t alone, so a warp finds it once for
+// all 8 x 4 pairs; where a scale's borders disagree, its blocks are rounded both ways and each code
+// takes its border's.  In steps of a mantissa: r, the
+// product and the border are off by less than 3 together, so seven or eight decide every such x, and no value
 // further than 24 from its border is moved over it; the next value of the type is at least 2^12
-// steps away.  Every lane of the warp calls it; gives Fp4Tensor::moves.
+// steps away.  Every lane of the warp calls it; gives Fp4Tensor::moves and ups.
 template <typename T>
-__device__ __forceinline__ uint32_t fp4_moves(float t) {
+__device__ __forceinline__ uint2 fp4_moves(float t) {
     constexpr int GRID = GridBits<T>::value;
     constexpr int mask = (1 << GRID) - 1;
     const int lane = threadIdx.x & 31;
@@ -174,16 +177,17 @@ __device__ __forceinline__ uint32_t fp4_moves(float t) {
     const int g = (b + (mask + 1) / 2) & ~mask;              // the type's value nearest to d m
     const float e = __fmaf_rn(-m, d, __int_as_float(g));     // its side, exactly
     const bool near = abs(g - b) <= 24;
-    const uint32_t up = __ballot_sync(0xffffffffu, near && e > 0.0f);
-    const uint32_t down = __ballot_sync(0xffffffffu, near && e < 0.0f);
-    const uint32_t on = __ballot_sync(0xffffffffu, near && e == 0.0f);
+    // on the border: the even code, which is the lower one at mantissas 1 and 5/4, the upper at 3/2 and 7/4
+    const bool above = e > 0.0f || (e == 0.0f && (lane & 2));
+    const uint32_t up = __ballot_sync(0xffffffffu, near && above);
+    const uint32_t down = __ballot_sync(0xffffffffu, near && !above);
     const int sh = lane & 28;
     const bool u = (up >> sh & 15u) != 0u, w = (down >> sh & 15u) != 0u;
-    const int move = (on >> sh & 15u) != 0u || (u && w) ? 1 : u ? 7 : w ? -7 : 0;
-    return __reduce_or_sync(0xffffffffu, ((uint32_t)move & 15u) << sh);
+    const int move = u && w ? -8 : u ? 7 : w ? -7 : 0;
+    return make_uint2(__reduce_or_sync(0xffffffffu, ((uint32_t)move & 15u) << sh), up);
 }
 
-// The tensor's constants but for `moves`, which 16-bit values with a tensor scale need too.
+// The tensor's constants but for `moves` and `ups`, which 16-bit values with a tensor scale need too.
 __device__ __forceinline__ Fp4Tensor fp4_tensor(const float* tensor_scale) {
     Fp4Tensor p;
     p.t = tensor_scale ? __ldg(tensor_scale) : 1.0f;
@@ -197,7 +201,7 @@ __device__ __forceinline__ Fp4Tensor fp4_tensor(const float* tensor_scale) {
         p.c = 1.0f;
     }
     p.rc = reciprocal(p.c);
-    p.moves = 0u;
+    p.moves = p.ups = 0u;
     return p;
 }
 
@@ -217,7 +221,10 @@ __device__ __forceinline__ uint32_t nv_scale_byte(float amax, const Fp4Tensor& p
 struct Fp4Scale {
     uint32_t byte;
     float d, r;      // NV: x / d, r its reciprocal; MX: x * r
-    int mode;        // 0: x * r; 1: the rounded quotient; 2: by comparison; 3: every code is zero
+    // 0: x * r; 1: the rounded quotient, or, for 16-bit values under a tensor scale, r and r + 16 steps
+    // by border; 2: by comparison; 3: every code is zero
+    int mode;
+    uint32_t ups;    // mode 1 of the second kind: bit j: borders of mantissa 1 + j / 4 take the larger
 };
 
 // The scale of a block of type T's values, from its absmax as the bits of an fp32 number (above
@@ -228,13 +235,14 @@ struct Fp4Scale {
 // NV: s = e4m3(amax / c), d = fl(s t), code = e2m1(x / d).  With d = s, of four bits, the quotient is
 //     rounded correctly (reciprocal, one residual, one correction: see RowDivisor): off a border it
 //     is at least 2^-24 of it away, so its rounding never moves it onto one.  d = fl(s t) has 24
-//     bits.  There 16-bit values take x * (1 / d), moved where a border falls next to one of them (see
-//     fp4_moves), or else, as fp32 values do, the rounded quotient, and, where that is on a border,
-//     the quotient rounded to odd.
+//     bits.  There 16-bit values take x * (1 / d), moved where a border falls on or next to one of them
+//     (see fp4_moves); fp32 values the rounded quotient, and, where that is on a border, the quotient
+//     rounded to odd.
 template <typename T, bool NV, bool HAS_T>
 __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, const Fp4Tensor& p) {
     constexpr int GRID = GridBits<T>::value;
     Fp4Scale b;
+    b.ups = 0u;
     if (!NV) {
         b.byte = (uint32_t)max((int)(amax_bits >> 23) - 2, 0);
         b.r = __uint_as_float((254u - b.byte) << 23);   // 2^(127 - byte): exponent field 2 to 254
@@ -256,7 +264,8 @@ __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, const Fp4Tenso
         const uint32_t i4 = __float_as_uint(s) >> 18 & 28u;
         const int move = (int)(p.moves << (i4 ^ 28u)) >> 28;
         b.r = __int_as_float(__float_as_int(b.r) + move);
-        b.mode = move == 1 ? 1 : 0;
+        b.mode = move == -8 ? 1 : 0;
+        b.ups = p.ups >> i4;
     }
     // the rounded quotient of a block that its scale saturates might overflow
     if (b.byte >= 0x7Eu && amax > 16.0f * b.d) b.mode = 2;
@@ -298,6 +307,29 @@ __device__ __forceinline__ void fp4_codes(const float (&x)[16], const Fp4Scale& 
         return;
     }
     if (!NV) return;
+    if (MUL && b.mode == 1) {
+        // The codes are those of the smaller reciprocal; the larger one's differ where a value is next to
+        // a border, the one above code n: mantissa 1 at n = 0, 3/2 at 1, 5/4 at 2, 4, 6 and 7/4 at 3, 5.
+        constexpr uint32_t ONES = 0x11111111u;
+        const float r = __int_as_float(__float_as_int(b.r) + 16);
+        const uint32_t u0 = 0u - (b.ups & 1u), u1 = 0u - (b.ups >> 1 & 1u), u2 = 0u - (b.ups >> 2 & 1u),
+                       u3 = 0u - (b.ups >> 3 & 1u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float2 q = f2_unpack(mul2s_rn(f2_pack(x[8 * h + i], x[8 * h + i + 1]), r));
+                v[i] = q.x;
+                v[i + 1] = q.y;
+            }
+            const uint32_t lo = codes[h], hi = fp4_pack8(v), high = lo >> 1 | lo >> 2;   // bit 0: n > 1
+            const uint32_t even = (u1 & high) | (u0 & ~high), odd = (u3 & high) | (u2 & ~high);
+            const uint32_t take = (((odd & lo) | (even & ~lo)) & ONES) * 15u;
+            codes[h] = (hi & take) | (lo & ~take);
+        }
+        return;
+    }
     if (b.mode == 1) {
         const unsigned long long r2 = f2_pack(b.r, b.r), nd2 = f2_pack(-b.d, -b.d);
         // A quotient on a border may have been rounded there.  All borders are multiples of 1/4:

@@ -148,7 +148,11 @@ __global__ void __launch_bounds__(fp4f::THREADS)
         const int groups = (int)min(left, (int64_t)n_kb * BK) / 16;   // of sixteen k; even for MX
         const int total = rows * groups;
         Fp4Tensor t = fp4_tensor(HAS_T ? p.x_ts : nullptr);
-        if (HAS_T && GridBits<T>::value > 0) t.moves = fp4_moves<T>(t.t);
+        if (HAS_T && GridBits<T>::value > 0) {
+            const uint2 m = fp4_moves<T>(t.t);
+            t.moves = m.x;
+            t.ups = m.y;
+        }
         const T* x = static_cast<const T*>(p.x);
         for (int base = 0; base < total; base += THREADS) {
             const int i = base + tid;

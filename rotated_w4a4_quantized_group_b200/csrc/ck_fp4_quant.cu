@@ -160,13 +160,16 @@ __global__ void __launch_bounds__(fp4q::THREADS, 4)
     if (n == 0) return;
     Fp4Tensor t = fp4_tensor(HAS_T ? p.tensor_scale : nullptr);
     constexpr bool MOVES = NV && HAS_T && GridBits<T>::value > 0;
-    __shared__ uint32_t moves;
+    __shared__ uint2 moves;
     if (MOVES && tid < 32) {
-        const uint32_t m = fp4_moves<T>(t.t);
+        const uint2 m = fp4_moves<T>(t.t);
         if (tid == 0) moves = m;
     }
     __syncthreads();   // and the cleared scale tiles
-    if (MOVES) t.moves = moves;
+    if (MOVES) {
+        t.moves = moves.x;
+        t.ups = moves.y;
+    }
     const T* x = static_cast<const T*>(p.x);
 
     if (LAYOUT == COL) {

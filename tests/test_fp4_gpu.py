@@ -132,6 +132,21 @@ def test_nv_borders(dt, t):
 
 
 @DT
+def test_nv_borders_of_short_tensor_scales(dt):
+    """Tensor scales of few bits put whole sets of borders onto x's values: powers of two, and 1 / 2688 of a
+    16-bit absmax in fp32 and rounded to that type."""
+    g = _gen(5)
+    m = (1 + torch.randint(0, 128, (14,), generator=g) / 128).tolist() + \
+        (1 + torch.randint(0, 1024, (10,), generator=g) / 1024).tolist()
+    ts = [2.0 ** -9, 2.0, 1.5, 1.25, 1.75]
+    for i, a in enumerate(m):
+        t = torch.tensor(a) / 2688
+        ts += [t.item(), t.to(BF16 if i % 2 else F16).float().item(), a]
+    for t in ts:
+        test_nv_borders(dt, t)
+
+
+@DT
 def test_nv_scale_borders(dt):
     """Block maxima on and next to the borders between two E4M3 scales."""
     mid = torch.from_numpy((ref.E4M3[1:] + ref.E4M3[:-1]) / 2 * 6.0)

@@ -5,9 +5,9 @@
 //   dequantize: value = cvt(fl(fl(code * scale) * t))
 //
 // Both are one pass over memory: K * sizeof(x) + K / 2 + K / block bytes a row, 12.5 us for 8192 x 3840
-// bf16 at the measured copy rate.  Measured there: MX 15.2 us, NV with a tensor scale 19.3 (about 206
+// bf16 at the measured copy rate.  Measured there: MX 15.2 us, NV with a tensor scale 20 to 22 (about 206
 // instructions a thread and block, of them 50 for the scale: the integer pipe is 61% busy), back 13.9;
-// 4096 x 16384 fp32: NV 52 us (48 at the copy rate), column-major 74, back 51.
+// 4096 x 16384 fp32: NV 49 us (48 at the copy rate), column-major 55, back 51.
 // A CTA takes 128 rows x 128 channels, so that it owns whole 512-byte scale tiles and writes each
 // of them as one contiguous run from shared memory; a thread takes sixteen channels of a row (an
 // NV block, or half an MX block whose other half is its neighbour lane's), with the loads of
@@ -29,7 +29,7 @@ constexpr int COLS = 128;             // channels of a CTA's tile
 constexpr int LANES = COLS / 16;      // threads across a row
 constexpr int STEP = THREADS / LANES; // rows a pass of the CTA covers
 constexpr int PASSES = ROWS / STEP;
-constexpr int COL_CHUNK = 64;         // channels a column-major tile transposes at a time
+constexpr int COL_CHUNK = 64;         // channels of a column-major tile that are waited for at a time
 enum Layout { VEC = 0, ANY = 1, COL = 2 };
 }  // namespace fp4q
 
@@ -80,6 +80,15 @@ __device__ __forceinline__ void rows_of_block(const int32_t* offsets, int n_expe
             return;
         }
     }
+}
+
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {   // all but the last N groups
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Sixteen consecutive elements at p as loaded words, and as fp32 values.
@@ -173,32 +182,50 @@ __global__ void __launch_bounds__(fp4q::THREADS, 4)
     const T* x = static_cast<const T*>(p.x);
 
     if (LAYOUT == COL) {
-        // 64 channels x 128 rows at a time: rows are contiguous in memory, so a warp reads 128 of
-        // them of one channel in a run; a thread then takes sixteen channels of one row, lanes on
-        // neighbouring rows (no bank conflicts: the buffer's row index is fastest)
-        T* buf = reinterpret_cast<T*>(q_smem);                           // [COL_CHUNK][ROWS]
-        uint8_t* cbuf = q_smem + (size_t)COL_CHUNK * ROWS * sizeof(T);   // [ROWS][COLS / 2 + 16]
+        // Rows are contiguous in memory, so a warp copies 128 of them of one channel in a run; a thread then
+        // takes sixteen channels of one row, lanes on neighbouring rows (no bank conflicts: the buffer's
+        // row index is fastest).  The whole tile is asked for at once and quantized in pieces of 64
+        // channels as they arrive (4096 x 16384 fp32 to
+        // NV: 55 us; piece by piece through registers, with a buffer of one, 74; bf16 41 against 67).
+        T* buf = reinterpret_cast<T*>(q_smem);                      // [COLS][ROWS]
+        uint8_t* cbuf = q_smem + (size_t)COLS * ROWS * sizeof(T);   // [ROWS][COLS / 2 + 16]
         constexpr int CP = COLS / 2 + 16;
-        constexpr int PER = 16 / (int)sizeof(T);                         // elements of 16 bytes
+        constexpr int PER = 16 / (int)sizeof(T);                    // elements of 16 bytes
         const int kmax = (int)((p.K - k0) < COLS ? (p.K - k0) : COLS);
-        for (int c0 = 0; c0 < kmax; c0 += COL_CHUNK) {
-            const int nc = (kmax - c0) < COL_CHUNK ? (kmax - c0) : COL_CHUNK;
-            if (n == ROWS && reinterpret_cast<uintptr_t>(x + row0) % 16 == 0 &&
-                (p.sk * (int64_t)sizeof(T)) % 16 == 0) {
-                constexpr int N16 = ROWS / PER;
+        const bool wide = reinterpret_cast<uintptr_t>(x + row0) % 16 == 0 &&
+                          (p.sk * (int64_t)sizeof(T)) % 16 == 0;
+#pragma unroll
+        for (int c0 = 0; c0 < COLS; c0 += COL_CHUNK) {
+            constexpr int N16 = ROWS / PER;
+            if (wide && n == ROWS) {   // without the tests of a ragged tile: 61 us with them
 #pragma unroll 8
                 for (int i = tid; i < COL_CHUNK * N16; i += THREADS) {
-                    const int c = i / N16, m = (i % N16) * PER;
-                    if (c < nc)
-                        *reinterpret_cast<uint4*>(buf + c * ROWS + m) = __ldg(reinterpret_cast<const uint4*>(
-                            x + row0 + m + (k0 + c0 + c) * p.sk));
+                    const int c = c0 + i / N16, m = (i % N16) * PER;
+                    if (c < kmax) cp_async_16(buf + c * ROWS + m, x + row0 + m + (k0 + c) * p.sk);
+                }
+            } else if (wide) {
+                for (int i = tid; i < COL_CHUNK * N16; i += THREADS) {
+                    const int c = c0 + i / N16, m = (i % N16) * PER;
+                    T* dst = buf + c * ROWS + m;
+                    const T* src = x + row0 + m + (k0 + c) * p.sk;
+                    if (c < kmax && m + PER <= n) cp_async_16(dst, src);
+                    else if (c < kmax && m < n)
+                        for (int e = 0; e < n - m; ++e) dst[e] = src[e];
                 }
             } else {
-                for (int i = tid; i < nc * ROWS; i += THREADS) {
-                    const int c = i / ROWS, m = i % ROWS;
-                    if (m < n) buf[c * ROWS + m] = x[row0 + m + (k0 + c0 + c) * p.sk];
+                for (int i = tid; i < COL_CHUNK * ROWS; i += THREADS) {
+                    const int c = c0 + i / ROWS, m = i % ROWS;
+                    if (c < kmax && m < n) buf[c * ROWS + m] = x[row0 + m + (k0 + c) * p.sk];
                 }
             }
+            cp_async_commit();
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < COLS; c0 += COL_CHUNK) {
+            if (c0 >= kmax) break;
+            const int nc = (kmax - c0) < COL_CHUNK ? (kmax - c0) : COL_CHUNK;
+            if (c0 + COL_CHUNK < COLS) cp_async_wait<COLS / COL_CHUNK - 1>();
+            else cp_async_wait<0>();
             __syncthreads();
             if (NV) {
                 for (int i = tid; i < nc / 16 * ROWS; i += THREADS) {
@@ -206,7 +233,7 @@ __global__ void __launch_bounds__(fp4q::THREADS, 4)
                     if (r < n) {
                         float v[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = Elem<T>::to_f(buf[(g * 16 + j) * ROWS + r]);
+                        for (int j = 0; j < 16; ++j) v[j] = Elem<T>::to_f(buf[(c0 + g * 16 + j) * ROWS + r]);
                         uint32_t c[2];
                         const Fp4Scale b = fp4_scale<T, NV, HAS_T>(absmax16(v), t);
                         fp4_codes<T, NV, HAS_T>(v, b, c);
@@ -221,7 +248,7 @@ __global__ void __launch_bounds__(fp4q::THREADS, 4)
                         float v[2][16];
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            v[j >> 4][j & 15] = Elem<T>::to_f(buf[(g * 32 + j) * ROWS + r]);
+                            v[j >> 4][j & 15] = Elem<T>::to_f(buf[(c0 + g * 32 + j) * ROWS + r]);
                         const Fp4Scale b = fp4_scale<T, NV, HAS_T>(max(absmax16(v[0]), absmax16(v[1])), t);
                         put_scale<NV>(sf, r, c0 / 16 + 2 * g, b.byte);
 #pragma unroll
@@ -233,8 +260,8 @@ __global__ void __launch_bounds__(fp4q::THREADS, 4)
                     }
                 }
             }
-            __syncthreads();
         }
+        __syncthreads();
         // the rows' codes, eight bytes a thread
         const int pieces = kmax / 16;
         for (int i = tid; i < ROWS * LANES; i += THREADS) {
@@ -412,7 +439,7 @@ static ck_status quant_launch(const Fp4QuantParams& p, int64_t grid, cudaStream_
         fp4_quant_kernel<T, NV, HAS_T, VEC><<<(unsigned)grid, THREADS, 0, stream>>>(p);
     } else if (p.sm == 1 && p.M >= 32) {
         // the channel runs of at least 32 rows are worth the transposing buffer
-        constexpr int smem = COL_CHUNK * ROWS * (int)sizeof(T) + ROWS * (COLS / 2 + 16);
+        constexpr int smem = COLS * ROWS * (int)sizeof(T) + ROWS * (COLS / 2 + 16);
         auto kern = fp4_quant_kernel<T, NV, HAS_T, COL>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return CK_ERR_CUDA;

@@ -15,7 +15,7 @@
 //   - multiplies on the tensor cores, 128 channels x BN rows, as the weights arrive,
 //   - writes its partial sums to shared memory; after a cluster barrier each CTA adds its share of
 //     the tile over the S partials in rank order (no atomics) and stores it.
-// Measured, 3840 x 3840: one bf16 row to NV 7.2 us replayed back to back (10.2 with the quantizer and
+// Measured, 3840 x 3840: one bf16 row to NV 6.9 us replayed back to back (10.2 with the quantizer and
 // the persistent kernel), 32 rows to MX with the quantizer before it 7.6 (10.1); the weights alone are
 // 1.3 us of HBM.
 // Every CTA takes both cluster barriers whatever happened before them; every mbarrier wait is bounded.
@@ -398,7 +398,7 @@ bool fp4_few_takes(int64_t M, int64_t N, int64_t K, bool nv, bool ragged) {
 }
 
 // Rows x steps of 256 k up to which the tiles quantize for themselves.  Measured (3840 channels, replayed,
-// bf16): K = 3840, 8 rows: MX 6.9 us and NV 8.1 against 7.3 and 7.9 with the quantizer in a launch of its
+// bf16): K = 3840, 8 rows: MX 6.5 us and NV 7.3 against 7.3 and 7.9 with the quantizer in a launch of its
 // own; 16 rows: 8.1 and 9.7 against 7.3 and 7.9; but that launch also costs the host 3 us.
 bool fp4_few_fuses(int64_t M, int64_t K) {
     return M >= 1 && M <= 16 && M * ((K + fp4f::BK - 1) / fp4f::BK) <= 180;

@@ -86,6 +86,10 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
                  : "memory");
 }
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() {   // all but the last N groups
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -186,7 +190,9 @@ __global__ void __launch_bounds__(fp4q::THREADS, 4)
         // takes sixteen channels of one row, lanes on neighbouring rows (no bank conflicts: the buffer's
         // row index is fastest).  The whole tile is asked for at once and quantized in pieces of 64
         // channels as they arrive (4096 x 16384 fp32 to
-        // NV: 55 us; piece by piece through registers, with a buffer of one, 74; bf16 41 against 67).
+        // NV: 55 us; piece by piece through registers, with a buffer of one, 74; bf16 41 against 67).  Columns
+        // that are not aligned to 16 bytes are copied by 4 (15322 x 2304 fp16 to MX: 28 us), 16-bit ones of
+        // an odd pitch by elements (54).
         T* buf = reinterpret_cast<T*>(q_smem);                      // [COLS][ROWS]
         uint8_t* cbuf = q_smem + (size_t)COLS * ROWS * sizeof(T);   // [ROWS][COLS / 2 + 16]
         constexpr int CP = COLS / 2 + 16;
@@ -194,6 +200,7 @@ __global__ void __launch_bounds__(fp4q::THREADS, 4)
         const int kmax = (int)((p.K - k0) < COLS ? (p.K - k0) : COLS);
         const bool wide = reinterpret_cast<uintptr_t>(x + row0) % 16 == 0 &&
                           (p.sk * (int64_t)sizeof(T)) % 16 == 0;
+        const bool words = sizeof(T) == 4 || (reinterpret_cast<uintptr_t>(x + row0) % 4 == 0 && p.sk % 2 == 0);
 #pragma unroll
         for (int c0 = 0; c0 < COLS; c0 += COL_CHUNK) {
             constexpr int N16 = ROWS / PER;
@@ -211,6 +218,16 @@ __global__ void __launch_bounds__(fp4q::THREADS, 4)
                     if (c < kmax && m + PER <= n) cp_async_16(dst, src);
                     else if (c < kmax && m < n)
                         for (int e = 0; e < n - m; ++e) dst[e] = src[e];
+                }
+            } else if (words) {
+                constexpr int PER4 = 4 / (int)sizeof(T), N4 = ROWS / PER4;
+#pragma unroll 8
+                for (int i = tid; i < COL_CHUNK * N4; i += THREADS) {
+                    const int c = c0 + i / N4, m = (i % N4) * PER4;
+                    T* dst = buf + c * ROWS + m;
+                    const T* src = x + row0 + m + (k0 + c) * p.sk;
+                    if (c < kmax && m + PER4 <= n) cp_async_4(dst, src);
+                    else if (c < kmax && m < n) *dst = *src;
                 }
             } else {
                 for (int i = tid; i < COL_CHUNK * ROWS; i += THREADS) {

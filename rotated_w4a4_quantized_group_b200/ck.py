@@ -480,6 +480,18 @@ def _check_codes(t: torch.Tensor, what: str, shape: tuple):
                          f"{tuple(t.shape)} {t.dtype} strides {t.stride()}")
 
 
+def _pitch(t: torch.Tensor, what: str) -> int:
+    """Distance of a (rows, width) view's rows, which the library walks: at least a row (broadcast and
+    overlapping rows are refused).  A single row's is never used and may be anything."""
+    rows, width = t.shape[-2:]
+    ld = t.stride(-2)
+    if ld < width:
+        if rows > 1:
+            raise ValueError(f"{what}'s rows must not overlap: {rows} rows of {width} at a pitch of {ld}")
+        ld = width
+    return ld
+
+
 def _check_scales(t: torch.Tensor, what: str, nbytes: int):
     if t.dtype != torch.uint8 or t.numel() < nbytes or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous uint8 tensor of at least {nbytes} bytes; got "
@@ -546,7 +558,7 @@ def ck_quant_fp4(x: torch.Tensor, fmt: int, *, tensor_scale: torch.Tensor | None
     _launch("ck_quant_fp4", dev, (
         x.data_ptr(), dt, M, K, sm, sk, fmt, None if tensor_scale is None else tensor_scale.data_ptr(),
         None if offsets is None else offsets.data_ptr(), E, codes.data_ptr(),
-        max(codes.stride(0), half), scales.data_ptr()))
+        _pitch(codes, "codes"), scales.data_ptr()))
     return codes, scales
 
 
@@ -577,9 +589,9 @@ def ck_dequant_fp4(codes: torch.Tensor, scales: torch.Tensor, fmt: int, *,
         _check_out(out, M, K, codes)
     odt = _float_code(out, "out")
     _launch("ck_dequant_fp4", dev, (
-        codes.data_ptr(), max(codes.stride(0), half), scales.data_ptr(), M, K, fmt,
+        codes.data_ptr(), _pitch(codes, "codes"), scales.data_ptr(), M, K, fmt,
         None if tensor_scale is None else tensor_scale.data_ptr(),
-        None if offsets is None else offsets.data_ptr(), E, out.data_ptr(), odt, max(out.stride(0), K)))
+        None if offsets is None else offsets.data_ptr(), E, out.data_ptr(), odt, _pitch(out, "out")))
     return out
 
 
@@ -632,7 +644,7 @@ def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_sc
             raise ValueError("x holds fp4 codes: x_scales must be given")
         _check_scales(x_scales, "x_scales", fp4_scales_bytes(M, K, fmt, nE))
         # one row's pitch is never used, and need not be one that TMA could
-        sm, sk = (max(sm, half) if M > 1 else (half + 15) // 16 * 16), 1
+        sm, sk = (_pitch(x, "x") if M > 1 else (half + 15) // 16 * 16), 1
     else:
         x_scales = None
         if workspace is None:
@@ -650,14 +662,14 @@ def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_sc
         ldo = N
     else:
         _check_out(out, M, N, x)
-        ldo = max(out.stride(0), N)
+        ldo = _pitch(out, "out")
     odt = _float_code(out, "out")
     head = (x.data_ptr(), dt, M, K, sm, sk, fmt, None if x_scales is None else x_scales.data_ptr(),
             None if x_tensor_scale is None else x_tensor_scale.data_ptr())
     tail = (w_scales.data_ptr(), None if w_tensor_scale is None else w_tensor_scale.data_ptr(),
             None if bias is None else bias.data_ptr(), bdt, out.data_ptr(), odt, ldo,
             ws, wsb, None if dev_status is None else dev_status.data_ptr())
-    w_ld = max(w_strides[-2], half) if N > 1 else (half + 15) // 16 * 16
+    w_ld = _pitch(w, "w_codes") if N > 1 else (half + 15) // 16 * 16
     if nE:
         _launch("ck_fp4_expert_linear", dev, (
             *head, offsets.data_ptr(), E, w.data_ptr(), N, w_ld, w_strides[0], *tail))

@@ -1,0 +1,78 @@
+"""The host side of the fp4 calls where no GPU is needed: what ck.py hands to the library, and what it
+refuses.  Its launch is replaced by a record of the arguments, its device check by one that takes host
+tensors; nothing is launched."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from rotated_w4a4_quantized_group_b200 import build as ck_build
+from rotated_w4a4_quantized_group_b200 import ck
+
+MX, NV = ck.CK_MXFP4, ck.CK_NVFP4
+BOTH = pytest.mark.parametrize("fmt", [MX, NV], ids=["mx", "nv"])
+
+
+@pytest.fixture
+def launched(monkeypatch):
+    """The (entry point, arguments) that reach the library."""
+    ck_build.build()
+    ck.lib()
+    calls = []
+    monkeypatch.setattr(ck, "_bind", None)
+    monkeypatch.setattr(ck, "_on_device", lambda x, *ts: 0)
+    monkeypatch.setattr(ck, "_launch", lambda name, dev, args: calls.append((name, args)))
+    return calls
+
+
+def _u8(*shape):
+    return torch.zeros(*shape, dtype=torch.uint8)
+
+
+# ------------------------------------------------------------------- rows that overlap
+
+def _overlapping(fmt):
+    """Calls with a tensor whose rows lie on top of one another: walked at a pitch of whole rows, it would
+    lead past its memory."""
+    M, N, K = 8, 24, 128
+    x, codes, w = torch.zeros(M, K), _u8(M, K // 2), _u8(N, K // 2)
+    sx, sw = _u8(ck.fp4_scales_bytes(M, K, fmt)), _u8(ck.fp4_scales_bytes(N, K, fmt))
+    off = torch.tensor([0, 3, M], dtype=torch.int32)
+    sx2 = _u8(ck.fp4_scales_bytes(M, K, fmt, 2))
+    for row in (lambda r, c, dt=torch.uint8: torch.zeros(1, c, dtype=dt).expand(r, c),
+                lambda r, c, dt=torch.uint8: torch.zeros(r * c, dtype=dt).as_strided((r, c), (c - 1, 1))):
+        out = row(M, N, torch.float32)
+        yield "codes", lambda: ck.ck_quant_fp4(x, fmt, codes=row(M, K // 2))
+        yield "codes", lambda: ck.ck_dequant_fp4(row(M, K // 2), sx, fmt)
+        yield "out", lambda: ck.ck_dequant_fp4(codes, sx, fmt, out=row(M, K, torch.float32))
+        yield "x", lambda: ck.ck_fp4_linear(row(M, K // 2), w, sw, fmt, x_scales=sx)
+        yield "w_codes", lambda: ck.ck_fp4_linear(x, row(N, K // 2), sw, fmt)
+        yield "out", lambda: ck.ck_fp4_linear(x, w, sw, fmt, out=out)
+        yield "x", lambda: ck.ck_fp4_expert_linear(row(M, K // 2), off, _u8(2, N, K // 2), torch.stack([sw, sw]), fmt,
+                                                   x_scales=sx2)
+        yield "w_codes", lambda: ck.ck_fp4_expert_linear(x, off, torch.stack([w, w])[:, :1].expand(2, N, K // 2),
+                                                         torch.stack([sw, sw]), fmt)
+        yield "out", lambda: ck.ck_fp4_expert_linear(x, off, torch.stack([w, w]), torch.stack([sw, sw]), fmt, out=out)
+
+
+@BOTH
+def test_overlapping_rows_are_refused(launched, fmt):
+    for what, call in _overlapping(fmt):
+        with pytest.raises(ValueError, match=f"{what}'s rows must not overlap"):
+            call()
+    assert not launched
+
+
+@BOTH
+def test_a_single_rows_pitch_is_not_used(launched, fmt):
+    K, N = 128, 24
+    w, sw, sx = _u8(N, K // 2), _u8(ck.fp4_scales_bytes(N, K, fmt)), _u8(ck.fp4_scales_bytes(1, K, fmt))
+    codes, out = _u8(K // 2).expand(1, K // 2), torch.zeros(N).expand(1, N)
+    ck.ck_quant_fp4(torch.zeros(1, K), fmt, codes=codes)
+    ck.ck_dequant_fp4(codes, sx, fmt, out=torch.zeros(K).expand(1, K))
+    ck.ck_fp4_linear(codes, w, sw, fmt, x_scales=sx, out=out)
+    ck.ck_fp4_linear(torch.zeros(1, K), w[:1], sw, fmt)
+    names = [name for name, _ in launched]
+    assert names == ["ck_quant_fp4", "ck_dequant_fp4", "ck_fp4_linear", "ck_fp4_linear"]
+    for ldq in (launched[0][1][11], launched[1][1][1], launched[2][1][4], launched[3][1][11]):
+        assert ldq == K // 2

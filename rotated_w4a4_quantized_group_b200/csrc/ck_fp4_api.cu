@@ -166,4 +166,11 @@ ck_status ck_fp4_expert_linear(const void* x, ck_dtype x_dtype, int64_t M, int64
                    out_dtype, ldo, workspace, workspace_bytes, dev_status, stream);
 }
 
+void ck_internal_fp4_tile(int64_t M, int64_t N, int64_t K, ck_fp4_format format, int n_experts, int ragged,
+                          int* ctas, int* rows) {
+    const Fp4Shape s = fp4_gemm_shape(M, N, K, n_experts > 0 ? n_experts : 1);
+    *ctas = n_experts == 0 && fp4_few_takes(M, N, K, format == CK_NVFP4, ragged != 0) ? 0 : s.cg;
+    *rows = s.bn;
+}
+
 }  // extern "C"

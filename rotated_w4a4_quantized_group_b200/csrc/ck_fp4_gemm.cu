@@ -406,14 +406,18 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     } else if (CG == 2 && warp == WARP_MMA) {
         // ---------------------------------------------------------------- the other CTA's epilogue
         // tells rank 0 that this CTA has read an accumulator: an arrival that reaches the other SM
-        // waits for its thread's earlier stores, so the epilogue's warps leave it to this one
+        // waits for its thread's earlier stores, so the epilogue's warps leave it to this one.  Only
+        // for the accumulators that rank 0 fills again: it waits for those arrivals, while one of the
+        // last two tiles' might reach its shared memory after it has left
         grid_dependency_wait();
-        for (uint32_t lt = 0; lt < my_tiles; ++lt) {
+        for (uint32_t lt = 0; lt + 2 < my_tiles; ++lt) {
             const uint32_t acc = lt & 1u;
             if (!__all_sync(0xffffffffu, mbar_wait(&acc_read[acc], (lt >> 1) & 1u, &abort_flag, p.dev_status)))
                 break;
             if (lane == 0) mbar_arrive_remote(&acc_empty[acc], 0);
         }
+        // after a timeout rank 0 waits for none of them: they have come before the closing barrier
+        if (lane == 0) fence_cluster();
         __syncwarp();
     } else if (warp >= EPI_WARP0) {
         // ---------------------------------------------------------------- epilogue
@@ -494,10 +498,6 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
 
 // ------------------------------------------------------------------ host
 
-struct Fp4Shape {
-    int cg, bn;
-};
-
 // CTAs per tile and rows per tile, by the estimated cycles of the busiest unit.  A stage takes its
 // MMAs and scale copies (BN / 2 cycles per 64 k, 14 per copy) but never less than about 520, what its
 // waits and issues take; a tile a little more; the last tile's epilogue about 30 a row, and a pair
@@ -506,7 +506,9 @@ struct Fp4Shape {
 // 3840 x 3840 MX (HBM-bound): 38, 43, 32.  Pairs of 128 rows were never the best by more than 2%.
 // Tiles start at multiples of 64 rows, so that a tile's first scale column is even; 32 rows only where
 // one tile holds them all.
-static Fp4Shape choose_shape(int64_t M, int64_t N, int64_t num_kb, int n_experts, int sms) {
+Fp4Shape fp4_gemm_shape(int64_t M, int64_t N, int64_t K, int n_experts) {
+    const int64_t num_kb = (K + fp4g::BK - 1) / fp4g::BK;
+    const int sms = num_sms();
     static const Fp4Shape all[] = {{2, 192}, {1, 128}, {1, 64}, {1, 32}};
     const int64_t m = (M + n_experts - 1) / n_experts;   // rows of an expert, were they even
     Fp4Shape best = all[0];
@@ -574,8 +576,7 @@ ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream) {
     const int E = a.offsets ? a.n_experts : 1;
     const int64_t num_kb = (a.K + BK - 1) / BK;
     const int64_t k_tiles = fp4_k_tiles(a.K, a.nv);
-    const int sms = num_sms();
-    const Fp4Shape shape = choose_shape(a.M, a.N, num_kb, E, sms);
+    const Fp4Shape shape = fp4_gemm_shape(a.M, a.N, a.K, E);
     Fp4GemmParams p;
     p.M = a.M;
     p.N = a.N;
@@ -642,7 +643,7 @@ ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream) {
         if (st != CK_OK) return st;
     }
     // tiles of one matrix are known here; the experts' only on the device
-    int64_t units = sms / shape.cg;
+    int64_t units = num_sms() / shape.cg;
     if (!a.offsets) {
         const int64_t tiles = (int64_t)p.tiles_n * ((a.M + p.BN - 1) / p.BN);
         if (tiles < units) units = tiles;

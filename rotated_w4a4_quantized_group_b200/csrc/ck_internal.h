@@ -155,6 +155,10 @@ struct Fp4Product {
     int* dev_status;
 };
 ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream);   // ck_fp4_gemm.cu
+struct Fp4Shape {
+    int cg, bn;   // CTAs and rows of a tile
+};
+Fp4Shape fp4_gemm_shape(int64_t M, int64_t N, int64_t K, int n_experts);   // n_experts 1 without offsets
 // Few rows or few tiles of one matrix (ck_fp4_few.cu), where fp4_few_takes: from codes, or, where
 // fp4_few_fuses and a.codes is NULL, from the activations x, quantized on the way.
 bool fp4_few_takes(int64_t M, int64_t N, int64_t K, bool nv, bool ragged);
@@ -167,3 +171,9 @@ ck_status launch_copy_rows(const int8_t* src, int64_t ld_src, int8_t* dst, int64
                            int64_t rows, int64_t cols, cudaStream_t stream);
 
 }  // namespace ck
+
+// For the tests, which have to know that they reach a kernel: the CTAs and rows of a tile of the product
+// from codes (n_experts 0: one matrix), 0 CTAs for fp4_few_kernel.  ragged: 16-bit outputs that do not take
+// 16-byte stores.
+extern "C" void ck_internal_fp4_tile(int64_t M, int64_t N, int64_t K, ck_fp4_format format, int n_experts,
+                                     int ragged, int* ctas, int* rows);

@@ -76,3 +76,19 @@ def test_a_single_rows_pitch_is_not_used(launched, fmt):
     assert names == ["ck_quant_fp4", "ck_dequant_fp4", "ck_fp4_linear", "ck_fp4_linear"]
     for ldq in (launched[0][1][11], launched[1][1][1], launched[2][1][4], launched[3][1][11]):
         assert ldq == K // 2
+
+
+# ------------------------------------------------------------------- the tests' own reach
+
+@BOTH
+def test_shapes_of_the_tile_tests_get_their_tiles(fmt):
+    """The GPU tests of one tile shape reach it by the library's rule, here too, where a change of the rule
+    shows at once."""
+    import test_fp4_tiles_gpu as t
+
+    ck_build.build()
+    for want, M, N, K in t.LINEARS:
+        for ragged in (False, True):
+            assert t.tile(M, N, t.width(K, fmt), fmt, ragged=ragged) == want, (M, N, K)
+    for want, off, N, K in t.EXPERTS:
+        assert t.tile(off[-1] + 9, N, t.width(K, fmt), fmt, len(off) - 1) == want, (off, N, K)

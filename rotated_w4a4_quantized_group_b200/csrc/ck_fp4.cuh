@@ -49,6 +49,18 @@ __host__ __device__ inline int64_t expert_scale_block(int64_t lo, int e) {
     return lo / kFp4TileRows + e;
 }
 
+// Counts of tiles added up, at most the largest int.  Offsets that do not decrease give fewer (the host
+// sees to that); others may give half of the experts all the rows, and a sum that wrapped would lead
+// out of the tensors.  Still associative: every partial sum is the true one or the largest int.
+__host__ __device__ inline int tiles_add(int a, int b) {
+    const uint32_t s = (uint32_t)a + (uint32_t)b;
+    return s > 0x7FFFFFFFu ? 0x7FFFFFFF : (int)s;
+}
+// Of `tiles`, those that unit u of `units` takes: u, u + units, ...
+__host__ __device__ inline uint32_t tiles_of_unit(int tiles, int u, int units) {
+    return tiles > u ? ((uint32_t)(tiles - u) + (uint32_t)units - 1u) / (uint32_t)units : 0u;
+}
+
 // Eight values -> eight E2M1 codes, the first in the lowest nibble: round half to even,
 // saturating at +-6.
 __device__ __forceinline__ uint32_t fp4_pack8(const float (&v)[8]) {

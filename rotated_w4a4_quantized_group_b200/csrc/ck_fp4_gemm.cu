@@ -245,14 +245,15 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
                 }
                 n = (int)((m + p.BN - 1) / p.BN) * p.tiles_n;
             }
-            int sum = n;
+            int sum = n;   // this expert's and those before it of the 32
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += o;
+                if (lane >= d) sum = tiles_add(sum, o);
             }
-            if (e < p.n_experts) cum[e] = before + sum - n;
-            before += __shfl_sync(0xffffffffu, sum, 31);
+            const int others = __shfl_up_sync(0xffffffffu, sum, 1);
+            if (e < p.n_experts) cum[e] = lane ? tiles_add(before, others) : before;
+            before = tiles_add(before, __shfl_sync(0xffffffffu, sum, 31));
         }
         if (lane == 0) cum[p.n_experts] = before;
     }
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
     // bytes of a stage that a producer of one CTA loads
     auto part_bytes = [&](int part) { return part == 0 ? A_BYTES : part == 1 ? p.b_bytes : SFA_BYTES + SFB_BYTES; };
     const uint32_t full0 = CG == 2 ? cluster_address(&full[0], 0) : smem_u32(&full[0]);
-    const uint32_t my_tiles = tiles > unit ? (uint32_t)((tiles - unit + units - 1) / units) : 0u;
+    const uint32_t my_tiles = tiles_of_unit(tiles, unit, units);
 
     if (warp == WARP_TMA_W || warp == WARP_TMA_X || warp == WARP_TMA_S) {
         // ---------------------------------------------------------------- loads
@@ -584,7 +585,8 @@ ck_status launch_fp4_gemm(const Fp4Product& a, cudaStream_t stream) {
     p.k64 = (int)((a.K + 63) / 64);
     p.BN = shape.bn;
     p.tiles_n = (int)((a.N + BW * shape.cg - 1) / (BW * shape.cg));
-    // the tile count stays an int: rows split over experts give at most one more tile each
+    // the tile count stays an int: rows split over experts give at most one more tile each (and one
+    // expert's alone, for offsets that decrease: see tiles_add)
     if ((double)p.tiles_n * ((double)a.M / p.BN + E + 1) >= 2147483647.0) return CK_ERR_UNSUPPORTED;
     p.b_bytes = (uint32_t)(shape.bn / shape.cg) * (BK / 2);
     const uint32_t sf_bytes = (a.nv ? 4 : 2) * kFp4TileBytes * (1 + shape.cg);

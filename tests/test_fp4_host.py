@@ -3,6 +3,8 @@ refuses.  Its launch is replaced by a record of the arguments, its device check 
 tensors; nothing is launched."""
 from __future__ import annotations
 
+import subprocess
+
 import pytest
 import torch
 
@@ -76,6 +78,53 @@ def test_a_single_rows_pitch_is_not_used(launched, fmt):
     assert names == ["ck_quant_fp4", "ck_dequant_fp4", "ck_fp4_linear", "ck_fp4_linear"]
     for ldq in (launched[0][1][11], launched[1][1][1], launched[2][1][4], launched[3][1][11]):
         assert ldq == K // 2
+
+
+# ------------------------------------------------------------------- counts of tiles
+
+COUNTS = r"""
+#include <cstdio>
+#include <vector>
+#include "ck_fp4.cuh"
+// experts' counts, lines of "n c0 c1 ...", added up in order and as a tree; then what the units take of them
+int main() {
+    int n;
+    while (std::scanf("%d", &n) == 1) {
+        std::vector<int> c(n);
+        for (int& v : c) std::scanf("%d", &v);
+        int sum = 0;
+        for (int v : c) sum = ck::tiles_add(sum, v);
+        std::vector<int> t = c;
+        for (size_t d = 1; d < t.size(); d *= 2)
+            for (size_t i = 0; i + d < t.size(); i += 2 * d) t[i] = ck::tiles_add(t[i], t[i + d]);
+        unsigned long long taken = 0;
+        unsigned last = 0;
+        for (int u = 0; u < 148; ++u) {
+            const unsigned k = ck::tiles_of_unit(sum, u, 148);
+            taken += k;
+            if (k && u + (k - 1) * 148ull > last) last = u + (k - 1) * 148ull;
+        }
+        std::printf("%d %d %llu %u\n", sum, t[0], taken, last);
+    }
+}
+"""
+
+
+def test_counts_of_tiles_never_wrap(tmp_path):
+    """Offsets that decrease can give half of the experts all the rows: the sum stays an int, and the units
+    take each tile once, none behind the last."""
+    src, exe = tmp_path / "counts.cu", tmp_path / "counts"
+    src.write_text(COUNTS)
+    subprocess.run([ck_build.nvcc(), "-std=c++17", "-I" + ck_build.INCLUDE, "-I" + ck_build.CSRC, *ck_build.ARCH,
+                    "-o", str(exe), str(src)], check=True)
+    top = 2 ** 31 - 1
+    cases = [[5, 0, 7], [0], [1] * 300, [1024 * 4096, 0] * 512, [top], [top, 1], [1, top, top], [top - 1, 1, 0],
+             [2 ** 30, 2 ** 30], [2 ** 30, 2 ** 30 - 1, 0, 3]]
+    text = "".join(f"{len(c)} {' '.join(map(str, c))}\n" for c in cases)
+    got = subprocess.run([str(exe)], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
+    for c, line in zip(cases, got):
+        want = min(sum(c), top)
+        assert [int(v) for v in line.split()] == [want, want, want, max(want - 1, 0)], c
 
 
 # ------------------------------------------------------------------- the tests' own reach

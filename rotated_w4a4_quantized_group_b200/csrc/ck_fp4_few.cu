@@ -408,7 +408,8 @@ template <typename T, bool NV, bool HAS_T, bool FUSED, bool RING>
 static ck_status few_launch_ring(const CUtensorMap* maps, const Fp4FewParams& p, int S, int tiles_n, size_t smem,
                             bool dep, cudaStream_t stream) {
     auto kern = fp4_few_kernel<T, NV, HAS_T, FUSED, RING>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    // the most that any call takes, not this call's: another thread may be about to launch a larger one
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fp4f::SMEM_BUDGET) != cudaSuccess)
         return CK_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];

@@ -534,7 +534,8 @@ template <typename OutT, bool NV, int CG>
 static ck_status fp4_launch(const CUtensorMap* maps, const Fp4GemmParams& p, size_t smem, int grid,
                             bool dep, cudaStream_t stream) {
     auto kern = fp4_gemm_kernel<OutT, NV, CG>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    // the most that any call takes, not this call's: another thread may be about to launch a larger one
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fp4g::SMEM_MAX) != cudaSuccess)
         return CK_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];

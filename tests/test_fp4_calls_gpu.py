@@ -3,14 +3,19 @@ threads at once, and after a call that failed."""
 from __future__ import annotations
 
 import ctypes
+import os
+import shutil
+import subprocess
 import threading
 
 import pytest
 import torch
 
+from rotated_w4a4_quantized_group_b200 import build as ck_build
 from rotated_w4a4_quantized_group_b200 import ck
 from rotated_w4a4_quantized_group_b200 import workloads as W
 from test_fp4_gpu import BF16, FMT
+from test_fp4_tiles_gpu import tile
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +115,70 @@ def test_the_first_int4_call_of_a_host_thread(M):
     got = _in_a_new_thread(f)
     assert not isinstance(got, Exception), got
     assert torch.equal(got, want)
+
+
+HAMMER = r"""
+#include <thread>
+#include "ck.h"
+// One thread per call: the call again and again, on a stream of its own; returns how many did not return CK_OK.
+struct Call {
+    const void* x; long long M, K, sm; int fmt; const unsigned char* xs; const unsigned char* w; long long N, w_ld;
+    const unsigned char* ws; void* out; cudaStream_t stream; int bad;
+};
+extern "C" void hammer(decltype(&ck_fp4_linear) fn, Call* c, int n, int times) {
+    std::thread t[8];
+    for (int i = 0; i < n; ++i)
+        t[i] = std::thread([=] {
+            for (int k = 0; k < times; ++k)
+                c[i].bad += fn(c[i].x, CK_FP4, c[i].M, c[i].K, c[i].sm, 1, (ck_fp4_format)c[i].fmt, c[i].xs, nullptr,
+                               c[i].w, c[i].N, c[i].w_ld, c[i].ws, nullptr, nullptr, CK_F32, c[i].out, CK_BF16, c[i].N,
+                               nullptr, 0, nullptr, c[i].stream) != CK_OK;
+        });
+    for (int i = 0; i < n; ++i) t[i].join();
+}
+"""
+
+
+class _Call(ctypes.Structure):
+    _fields_ = [(n, t) for n, t in zip(
+        ("x", "M", "K", "sm", "fmt", "xs", "w", "N", "w_ld", "ws", "out", "stream", "bad"),
+        (ctypes.c_void_p, ctypes.c_longlong, ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p,
+         ctypes.c_void_p, ctypes.c_longlong, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+         ctypes.c_int))]
+
+
+@pytest.fixture(scope="module")
+def hammer(tmp_path_factory):
+    d = tmp_path_factory.mktemp("hammer")
+    (d / "hammer.cpp").write_text(HAMMER)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(ck_build.nvcc())), "include")
+    subprocess.run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-pthread", "-I" + cuda,
+                    "-I" + ck_build.INCLUDE, str(d / "hammer.cpp"), "-o", str(d / "hammer.so")], check=True)
+    return ctypes.CDLL(str(d / "hammer.so")).hammer
+
+
+@FMT
+@pytest.mark.parametrize("tiles,shapes", [(((0, 64), (0, 64)), ((33, 128, 2048), (33, 128, 12288))),
+                                          (((1, 64), (1, 128)), ((400, 1600, 1024), (900, 2100, 768)))],
+                         ids=["few tiles", "one CTA a tile"])
+def test_host_threads_with_different_sizes(hammer, fmt, tiles, shapes):
+    """Two threads launch one kernel with different amounts of shared memory: neither takes the other's
+    allowance away between its being set and the launch."""
+    for t, s in zip(tiles, shapes):
+        ctas, rows = tile(*s, fmt)
+        assert ctas == t[0] and (ctas == 0 or rows == t[1])
+    calls, keep = (_Call * 2)(), []
+    for i, (M, N, K) in enumerate(shapes):
+        g = torch.Generator(device="cuda").manual_seed(140 + i)
+        x, xs = ck.ck_quant_fp4(torch.randn(M, K, device="cuda", generator=g), fmt)
+        w, ws = ck.ck_quant_fp4(torch.randn(N, K, device="cuda", generator=g) * 0.05, fmt)
+        out, stream = torch.empty(M, N, dtype=BF16, device="cuda"), torch.cuda.Stream()
+        keep.append((x, xs, w, ws, out, stream, ck.ck_fp4_linear(x, w, ws, fmt, x_scales=xs, out_dtype=BF16)))
+        calls[i] = _Call(x.data_ptr(), M, K, x.stride(0), fmt, xs.data_ptr(), w.data_ptr(), N, w.stride(0),
+                         ws.data_ptr(), out.data_ptr(), stream.cuda_stream, 0)
+    torch.cuda.synchronize()
+    hammer(ctypes.cast(ck.lib().ck_fp4_linear, ctypes.c_void_p), calls, 2, 50000)
+    torch.cuda.synchronize()
+    assert [c.bad for c in calls] == [0, 0]
+    for *_, out, _, want in keep:
+        assert torch.equal(out, want)

@@ -410,7 +410,7 @@ static ck_status few_launch_ring(const CUtensorMap* maps, const Fp4FewParams& p,
     auto kern = fp4_few_kernel<T, NV, HAS_T, FUSED, RING>;
     // the most that any call takes, not this call's: another thread may be about to launch a larger one
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fp4f::SMEM_BUDGET) != cudaSuccess)
-        return CK_ERR_CUDA;
+        return cuda_error();
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -425,8 +425,7 @@ static ck_status few_launch_ring(const CUtensorMap* maps, const Fp4FewParams& p,
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = dep ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p) != cudaSuccess) return CK_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? CK_OK : CK_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p) == cudaSuccess ? CK_OK : cuda_error();
 }
 
 template <typename T, bool NV, bool HAS_T, bool FUSED>

@@ -536,7 +536,7 @@ static ck_status fp4_launch(const CUtensorMap* maps, const Fp4GemmParams& p, siz
     auto kern = fp4_gemm_kernel<OutT, NV, CG>;
     // the most that any call takes, not this call's: another thread may be about to launch a larger one
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fp4g::SMEM_MAX) != cudaSuccess)
-        return CK_ERR_CUDA;
+        return cuda_error();
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     int n = 0;
@@ -558,9 +558,7 @@ static ck_status fp4_launch(const CUtensorMap* maps, const Fp4GemmParams& p, siz
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = (unsigned)n;
-    if (cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p) != cudaSuccess)
-        return CK_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? CK_OK : CK_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p) == cudaSuccess ? CK_OK : cuda_error();
 }
 
 template <typename OutT>

@@ -448,23 +448,32 @@ static int64_t row_blocks(int64_t M, const int32_t* offsets, int n_experts) {
     return offsets ? M / kFp4TileRows + n_experts : (M + kFp4TileRows - 1) / kFp4TileRows;
 }
 
+// Launched so that the launch's own status is returned, not what an earlier call left as the last error.
+template <typename P>
+static ck_status launch(void (*kern)(P), const P& p, int64_t grid, int smem, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(fp4q::THREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? CK_OK : cuda_error();
+}
+
 template <typename T, bool NV, bool HAS_T>
 static ck_status quant_launch(const Fp4QuantParams& p, int64_t grid, cudaStream_t stream) {
     using namespace fp4q;
     const int64_t eb = sizeof(T);
-    if (p.sk == 1 && aligned(p.x, 16) && p.sm * eb % 16 == 0) {
-        fp4_quant_kernel<T, NV, HAS_T, VEC><<<(unsigned)grid, THREADS, 0, stream>>>(p);
-    } else if (p.sm == 1 && p.M >= 32) {
+    if (p.sk == 1 && aligned(p.x, 16) && p.sm * eb % 16 == 0)
+        return launch(fp4_quant_kernel<T, NV, HAS_T, VEC>, p, grid, 0, stream);
+    if (p.sm == 1 && p.M >= 32) {
         // the channel runs of at least 32 rows are worth the transposing buffer
         constexpr int smem = COLS * ROWS * (int)sizeof(T) + ROWS * (COLS / 2 + 16);
         auto kern = fp4_quant_kernel<T, NV, HAS_T, COL>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return CK_ERR_CUDA;
-        kern<<<(unsigned)grid, THREADS, smem, stream>>>(p);
-    } else {
-        fp4_quant_kernel<T, NV, HAS_T, ANY><<<(unsigned)grid, THREADS, 0, stream>>>(p);
+            return cuda_error();
+        return launch(kern, p, grid, smem, stream);
     }
-    return cudaGetLastError() == cudaSuccess ? CK_OK : CK_ERR_CUDA;
+    return launch(fp4_quant_kernel<T, NV, HAS_T, ANY>, p, grid, 0, stream);
 }
 
 template <typename T>
@@ -505,9 +514,9 @@ ck_status launch_quant_fp4(const void* x, ck_dtype dt, int64_t M, int64_t K, int
 }
 
 template <typename T>
-static void dequant_typed(const Fp4DequantParams& p, bool nv, int64_t grid, cudaStream_t stream) {
-    if (nv) fp4_dequant_kernel<T, true><<<(unsigned)grid, fp4q::THREADS, 0, stream>>>(p);
-    else fp4_dequant_kernel<T, false><<<(unsigned)grid, fp4q::THREADS, 0, stream>>>(p);
+static ck_status dequant_typed(const Fp4DequantParams& p, bool nv, int64_t grid, cudaStream_t stream) {
+    return nv ? launch(fp4_dequant_kernel<T, true>, p, grid, 0, stream)
+              : launch(fp4_dequant_kernel<T, false>, p, grid, 0, stream);
 }
 
 ck_status launch_dequant_fp4(const uint8_t* codes, int64_t ldq, const uint8_t* scales, int64_t M,
@@ -534,12 +543,11 @@ ck_status launch_dequant_fp4(const uint8_t* codes, int64_t ldq, const uint8_t* s
     if (grid >= (1LL << 31)) return CK_ERR_UNSUPPORTED;
     p.col_ctas = (int)cols;
     switch (out_dt) {
-        case CK_F32: dequant_typed<float>(p, nv, grid, stream); break;
-        case CK_F16: dequant_typed<__half>(p, nv, grid, stream); break;
-        case CK_BF16: dequant_typed<__nv_bfloat16>(p, nv, grid, stream); break;
+        case CK_F32: return dequant_typed<float>(p, nv, grid, stream);
+        case CK_F16: return dequant_typed<__half>(p, nv, grid, stream);
+        case CK_BF16: return dequant_typed<__nv_bfloat16>(p, nv, grid, stream);
         default: return CK_ERR_INVALID_ARG;
     }
-    return cudaGetLastError() == cudaSuccess ? CK_OK : CK_ERR_CUDA;
 }
 
 }  // namespace ck

@@ -17,6 +17,13 @@ ck_status encode_tma(CUtensorMap* map, CUtensorMapDataType dtype, int rank, cons
 
 int num_sms();
 
+// A runtime call failed.  What it leaves behind as the last error is taken back: the check behind a later
+// launch would find it there.
+inline ck_status cuda_error() {
+    cudaGetLastError();
+    return CK_ERR_CUDA;
+}
+
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Where stage 2 writes its outputs: channels [start[s], start[s + 1]) go to segment s, whose

@@ -182,3 +182,28 @@ def test_host_threads_with_different_sizes(hammer, fmt, tiles, shapes):
     assert [c.bad for c in calls] == [0, 0]
     for *_, out, _, want in keep:
         assert torch.equal(out, want)
+
+
+@FMT
+@pytest.mark.parametrize("M", [4, 40, 100, 3000])
+def test_a_failed_call_is_not_the_next_ones_fault(fmt, M):
+    """A launch into a capture that something else has ended fails on the host; the next call, elsewhere, is
+    right and says so."""
+    call, out, want = _linear(M, 907, 4096, fmt, 150, M > 16)
+    x = torch.randn(64, 128, device="cuda", dtype=BF16)
+    cudart = ctypes.CDLL("libcudart.so.12")
+    stream = torch.cuda.Stream()
+    handle = ctypes.c_void_p(stream.cuda_stream)
+    for after in (lambda: call(torch.cuda.current_stream().cuda_stream), lambda: ck.ck_quant_fp4(x, fmt) and ck.CK_OK):
+        torch.cuda.synchronize()
+        assert cudart.cudaStreamBeginCapture(handle, 2) == 0             # relaxed
+        assert cudart.cudaStreamSynchronize(handle) != 0                 # not allowed there: the capture is void
+        failed = call(stream.cuda_stream)
+        graph = ctypes.c_void_p()
+        assert cudart.cudaStreamEndCapture(handle, ctypes.byref(graph)) != 0
+        cudart.cudaGetLastError()
+        assert failed == ck.CK_ERR_CUDA
+        assert after() == ck.CK_OK
+    assert call(torch.cuda.current_stream().cuda_stream) == ck.CK_OK
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

@@ -276,7 +276,8 @@ ck_status ck_rotate_quant_packed(const void* x, ck_dtype x_dtype, int64_t M, int
  * cores take: row r, block c of a tile at byte (r % 32) * 16 + (r / 32) * 4 + c; the tile of rows
  * 128 i.. and blocks 4 j.. at byte (i * ceil(blocks / 4) + j) * 512.  With rows sorted by expert
  * (offsets, below) expert e's rows start a tile row of their own, i = offsets[e] / 128 + e.
- * Scale pointers are 16-byte aligned.
+ * Scale pointers are 16-byte aligned; every other pointer of the fp4 calls is a multiple of its type's size
+ * where nothing more is said (CK_ERR_INVALID_ARG otherwise).
  */
 typedef enum { CK_MXFP4 = 0, CK_NVFP4 = 1 } ck_fp4_format;
 

@@ -13,6 +13,8 @@ static constexpr int64_t kTileRows = 128, kTileBytes = 512;
 
 static bool fp4_float(ck_dtype d) { return d == CK_F32 || d == CK_F16 || d == CK_BF16; }
 static bool fp4_format(ck_fp4_format f) { return f == CK_MXFP4 || f == CK_NVFP4; }
+// On an address that the type's elements can have (NULL is one).
+static bool fp4_at(const void* p, ck_dtype d) { return aligned(p, d == CK_F32 ? 4 : d == CK_FP4 ? 1 : 2); }
 static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 static int64_t fp4_block_of(ck_fp4_format f) { return f == CK_NVFP4 ? 16 : 32; }
 // Sizes beyond these are refused before any of them is multiplied.
@@ -44,6 +46,9 @@ static ck_status product(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, 
     if (!x || !w || !w_scales || !out || (codes_in && !x_scales)) return CK_ERR_INVALID_ARG;
     if (!aligned(w, 16) || !aligned(w_scales, 16)) return CK_ERR_INVALID_ARG;
     if (codes_in && (!aligned(x, 16) || !aligned(x_scales, 16))) return CK_ERR_INVALID_ARG;
+    if (!fp4_at(x, x_dtype) || !fp4_at(out, out_dtype) || (bias && !fp4_at(bias, bias_dtype)) ||
+        !aligned(x_ts, 4) || !aligned(w_ts, 4) || !aligned(offsets, 4) || !aligned(dev_status, 4))
+        return CK_ERR_INVALID_ARG;
     if (M >= (1LL << 31) || N >= (1LL << 31) || K >= (1LL << 31)) return CK_ERR_UNSUPPORTED;
 
     Fp4Product a = {};
@@ -115,7 +120,9 @@ ck_status ck_quant_fp4(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, in
         (offsets && (n_experts < 1 || n_experts > kMaxExperts)))
         return CK_ERR_INVALID_ARG;
     if (M == 0) return CK_OK;
-    if (!x || !codes || !scales || !aligned(scales, 16)) return CK_ERR_INVALID_ARG;
+    if (!x || !codes || !scales || !aligned(scales, 16) || !fp4_at(x, x_dtype) ||
+        !aligned(tensor_scale, 4) || !aligned(offsets, 4))
+        return CK_ERR_INVALID_ARG;
     if (!fp4_sizes(M, K, format)) return CK_ERR_UNSUPPORTED;
     return launch_quant_fp4(x, x_dtype, M, K, stride_m, stride_k, format == CK_NVFP4, tensor_scale,
                             offsets, n_experts, codes, ldq, scales, stream);
@@ -131,7 +138,9 @@ ck_status ck_dequant_fp4(const uint8_t* codes, int64_t ldq, const uint8_t* scale
         (offsets && (n_experts < 1 || n_experts > kMaxExperts)))
         return CK_ERR_INVALID_ARG;
     if (M == 0) return CK_OK;
-    if (!codes || !scales || !out || !aligned(scales, 16)) return CK_ERR_INVALID_ARG;
+    if (!codes || !scales || !out || !aligned(scales, 16) || !fp4_at(out, out_dtype) ||
+        !aligned(tensor_scale, 4) || !aligned(offsets, 4))
+        return CK_ERR_INVALID_ARG;
     if (!fp4_sizes(M, K, format)) return CK_ERR_UNSUPPORTED;
     return launch_dequant_fp4(codes, ldq, scales, M, K, format == CK_NVFP4, tensor_scale, offsets,
                               n_experts, out, out_dtype, ldo, stream);

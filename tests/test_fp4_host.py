@@ -80,6 +80,39 @@ def test_a_single_rows_pitch_is_not_used(launched, fmt):
         assert ldq == K // 2
 
 
+# ------------------------------------------------------------------- addresses
+
+ODD = [("quant", dict(x=1)), ("quant", dict(dt=ck.CK_F32, x=2)), ("quant", dict(ts=2)), ("quant", dict(off=2, E=2)),
+       ("dequant", dict(out=1)), ("dequant", dict(odt=ck.CK_F32, out=2)), ("dequant", dict(ts=1)),
+       ("dequant", dict(off=2, E=2)), ("linear", dict(x=1)), ("linear", dict(dt=ck.CK_F32, x=2)), ("linear", dict(out=1)),
+       ("linear", dict(odt=ck.CK_F32, out=2)), ("linear", dict(bias=2)), ("linear", dict(bdt=ck.CK_F16, bias=1)),
+       ("linear", dict(xts=2)), ("linear", dict(wts=2)), ("linear", dict(status=2)), ("linear", dict(M=4, x=1)),
+       ("experts", dict(off=2)), ("experts", dict(wts=1)), ("experts", dict(out=1)), ("experts", dict(status=1))]
+
+
+@pytest.mark.parametrize("fn,odd", ODD)
+def test_addresses_that_no_element_has_are_refused(fn, odd):
+    """A pointer that is not a multiple of its type's size would be a misaligned access on the device."""
+    ck_build.build()
+    L, P = ck.lib(), 1 << 20
+    a = dict(x=0, dt=ck.CK_BF16, M=40, E=3, off=None, ts=None, out=0, odt=ck.CK_BF16, xts=None, wts=None, bias=None,
+             bdt=ck.CK_F32, status=None)
+    a.update(odd)
+    at = {k: None if a[k] is None else P + a[k] for k in ("x", "off", "ts", "out", "xts", "wts", "bias", "status")}
+    if fn == "quant":
+        st = L.ck_quant_fp4(at["x"], a["dt"], a["M"], 64, 64, 1, NV, at["ts"], at["off"], a["E"], P, 32, P, None)
+    elif fn == "dequant":
+        st = L.ck_dequant_fp4(P, 32, P, a["M"], 64, NV, at["ts"], at["off"], a["E"], at["out"], a["odt"], 64, None)
+    else:
+        head = (at["x"], a["dt"], a["M"], 64, 64, 1, NV, None, at["xts"])
+        tail = (P, at["wts"], at["bias"], a["bdt"], at["out"], a["odt"], 8, P, 1 << 20, at["status"], None)
+        if fn == "linear":
+            st = L.ck_fp4_linear(*head, P, 8, 32, *tail)
+        else:
+            st = L.ck_fp4_expert_linear(*head, P if at["off"] is None else at["off"], 3, P, 8, 32, 256, *tail)
+    assert st == ck.CK_ERR_INVALID_ARG
+
+
 # ------------------------------------------------------------------- counts of tiles
 
 COUNTS = r"""

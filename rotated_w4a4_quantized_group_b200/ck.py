@@ -498,9 +498,16 @@ def _check_scales(t: torch.Tensor, what: str, nbytes: int):
                          f"{t.numel()} of {t.dtype}")
 
 
+def _check_memory(t: torch.Tensor, what: str):
+    if t.is_neg():
+        raise ValueError(f"{what} is a negated view, whose memory does not hold its values: pass "
+                         f"{what}.resolve_neg()")
+
+
 def _check_tensor_scale(t: torch.Tensor, what: str, n: int, fmt: int):
     if fmt == CK_MXFP4:
         raise ValueError(f"{what}: CK_MXFP4 has no tensor scale")
+    _check_memory(t, what)
     if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous fp32 tensor of {n} values; got {t.numel()} of "
                          f"{t.dtype}")
@@ -519,6 +526,7 @@ def _float_code(t: torch.Tensor, what: str) -> int:
     code = _FLOAT_CODE.get(t.dtype)
     if code is None:
         raise ValueError(f"{what} must be fp32, fp16 or bf16; got {t.dtype}")
+    _check_memory(t, what)
     return code
 
 
@@ -607,6 +615,7 @@ def _fp4_product(x, offsets, w, E, N, w_scales, fmt, bias, x_scales, x_tensor_sc
         if x.dtype != torch.uint8:
             raise ValueError(f"x must be fp32, fp16 or bf16, or uint8 codes; got {x.dtype}")
         dt, K = CK_FP4, 2 * K
+    _check_memory(x, "x")
     _check_fp4(fmt, K)
     dev = _on_device(x, w, w_scales, bias, x_tensor_scale, w_tensor_scale, offsets, out, x_scales,
                      workspace, dev_status)

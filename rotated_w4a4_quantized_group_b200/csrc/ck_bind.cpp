@@ -25,8 +25,11 @@ decltype(&ck_dequant_fp4) dequant_fp4;
 decltype(&ck_fp4_linear) fp4_linear;
 decltype(&ck_fp4_expert_linear) fp4_expert_linear;
 
-// An argument that may be None.  `ok` turns false where it is neither None nor a strided tensor on
-// device `dev`.
+// A strided CUDA tensor whose memory holds its values (a negated view's holds their negatives).
+bool in_memory(const at::Tensor& t) { return t.is_cuda() && t.layout() == at::kStrided && !t.is_neg(); }
+
+// An argument that may be None.  `ok` turns false where it is neither None nor such a tensor on device
+// `dev`.
 struct Arg {
     const at::Tensor* t = nullptr;
     void* ptr() const { return t ? t->data_ptr() : nullptr; }
@@ -39,7 +42,7 @@ Arg optional(PyObject* o, int dev, bool& ok) {
         return a;
     }
     a.t = &THPVariable_Unpack(o);
-    if (!a.t->is_cuda() || a.t->get_device() != dev || a.t->layout() != at::kStrided) ok = false;
+    if (!in_memory(*a.t) || a.t->get_device() != dev) ok = false;
     return a;
 }
 
@@ -47,7 +50,7 @@ Arg optional(PyObject* o, int dev, bool& ok) {
 const at::Tensor* on_current_device(PyObject* o, int& dev) {
     if (!THPVariable_Check(o)) return nullptr;
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.layout() != at::kStrided) return nullptr;
+    if (!in_memory(t)) return nullptr;
     dev = t.get_device();
     return dev == c10::cuda::current_device() ? &t : nullptr;
 }

@@ -207,3 +207,21 @@ def test_a_failed_call_is_not_the_next_ones_fault(fmt, M):
     assert call(torch.cuda.current_stream().cuda_stream) == ck.CK_OK
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_negated_views_are_refused_on_both_host_sides(monkeypatch):
+    M, N, K = 20, 64, 128
+    g = torch.Generator(device="cuda").manual_seed(170)
+    z = torch.randn(M, K, 2, device="cuda", generator=g)
+    plain, neg = torch.view_as_complex(z).imag, torch.view_as_complex(z).conj().imag
+    w, ws = ck.ck_quant_fp4(torch.randn(N, K, device="cuda", generator=g), ck.CK_NVFP4)
+    t = torch.view_as_complex(torch.ones(1, 2, device="cuda")).conj().imag
+    calls = [lambda v: ck.ck_quant_fp4(v, ck.CK_NVFP4)[0], lambda v: ck.ck_fp4_linear(v, w, ws, ck.CK_NVFP4)]
+    for bind in (ck._bind, None):
+        monkeypatch.setattr(ck, "_bind", bind)
+        for f in calls:
+            with pytest.raises(ValueError, match="negated view"):
+                f(neg)
+            assert torch.equal(f(neg.resolve_neg()), f(-plain)) and torch.equal(f(plain), f(plain.contiguous()))
+        with pytest.raises(ValueError, match="negated view"):
+            ck.ck_quant_fp4(plain, ck.CK_NVFP4, tensor_scale=t)

@@ -80,6 +80,32 @@ def test_a_single_rows_pitch_is_not_used(launched, fmt):
         assert ldq == K // 2
 
 
+# ------------------------------------------------------------------- values that are not in memory
+
+def test_negated_views_are_refused(launched):
+    """The imaginary part of a conjugate is a view whose memory holds the negatives of its values."""
+    def neg(*shape):
+        t = torch.view_as_complex(torch.ones(*shape, 2)).conj().imag
+        assert t.is_neg() and t.dtype == torch.float32
+        return t
+
+    M, N, K = 4, 24, 128
+    x, w, sw = torch.zeros(M, K), _u8(N, K // 2), _u8(ck.fp4_scales_bytes(N, K, NV))
+    codes, sx, t = _u8(M, K // 2), _u8(ck.fp4_scales_bytes(M, K, NV)), torch.ones(1)
+    for what, call in [
+            ("x", lambda: ck.ck_quant_fp4(neg(M, K), NV)),
+            ("tensor_scale", lambda: ck.ck_quant_fp4(x, NV, tensor_scale=neg(1))),
+            ("tensor_scale", lambda: ck.ck_dequant_fp4(codes, sx, NV, tensor_scale=neg(1))),
+            ("x", lambda: ck.ck_fp4_linear(neg(M, K), w, sw, NV)),
+            ("bias", lambda: ck.ck_fp4_linear(x, w, sw, NV, neg(N))),
+            ("x_tensor_scale", lambda: ck.ck_fp4_linear(x, w, sw, NV, x_tensor_scale=neg(1))),
+            ("w_tensor_scale", lambda: ck.ck_fp4_linear(x, w, sw, NV, x_tensor_scale=t, w_tensor_scale=neg(1))),
+            ("x", lambda: ck.ck_fp4_expert_linear(neg(M, K), torch.zeros(2, dtype=torch.int32), w[None], sw[None], NV))]:
+        with pytest.raises(ValueError, match=f"{what} is a negated view"):
+            call()
+    assert not launched
+
+
 # ------------------------------------------------------------------- addresses
 
 ODD = [("quant", dict(x=1)), ("quant", dict(dt=ck.CK_F32, x=2)), ("quant", dict(ts=2)), ("quant", dict(off=2, E=2)),

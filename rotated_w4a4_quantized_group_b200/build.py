@@ -88,21 +88,26 @@ def build(force: bool = False, variant=None) -> str:
 
 BIND_SRC = os.path.join(CSRC, "ck_bind.cpp")
 BIND = os.path.join(HERE, "_ck_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
+BIND_TORCH = "ck_bind.torch"    # in BUILD_DIR: the torch version that BIND was built against
 
 
 def build_bind(force: bool = False) -> str:
-    """The Python extension _ck_bind, which loads libck.so when it is told where."""
-    deps = [BIND_SRC, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(BIND) and \
-            all(os.path.getmtime(p) <= os.path.getmtime(BIND) for p in deps):
-        return BIND
+    """The Python extension _ck_bind, which loads libck.so when it is told where.  Built again for another
+    torch, whose types and symbols may differ."""
     import torch
 
+    deps = [BIND_SRC, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    stamp = os.path.join(BUILD_DIR, BIND_TORCH)
+    built_for = open(stamp).read() if os.path.exists(stamp) else None
+    if not force and built_for == str(torch.__version__) and os.path.exists(BIND) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(BIND) for p in deps):
+        return BIND
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = BIND + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DCK_TORCH_VERSION="{torch.__version__}"', "-I" + INCLUDE,
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(t, "include"),
            "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
            "-I" + os.path.join(cuda, "include"), BIND_SRC, "-o", tmp, "-L" + os.path.join(t, "lib"),
@@ -111,6 +116,9 @@ def build_bind(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BIND)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
     return BIND
 
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import warnings
 
 import torch
 
@@ -92,8 +93,13 @@ def lib() -> ctypes.CDLL:
         except ImportError:     # not built: the fp4 calls take Python's way, with the same results
             pass
         else:
-            _ck_bind.load(LIB_PATH)
-            _bind = _ck_bind
+            built_for = getattr(_ck_bind, "torch_version", None)
+            if built_for == str(torch.__version__):
+                _ck_bind.load(LIB_PATH)
+                _bind = _ck_bind
+            else:               # its view of a tensor may be another's
+                warnings.warn(f"_ck_bind was built against torch {built_for}, this is "
+                              f"{torch.__version__}: the fp4 calls do without it until the package is built again")
     return _lib
 
 

@@ -269,4 +269,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ck_bind", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ck_bind() { return PyModule_Create(&module); }
+// torch_version: what it was built against; ck.py uses it with no other.
+PyMODINIT_FUNC PyInit__ck_bind() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", CK_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -4,6 +4,7 @@ tensors; nothing is launched."""
 from __future__ import annotations
 
 import subprocess
+import warnings
 
 import pytest
 import torch
@@ -137,6 +138,50 @@ def test_addresses_that_no_element_has_are_refused(fn, odd):
         else:
             st = L.ck_fp4_expert_linear(*head, P if at["off"] is None else at["off"], 3, P, 8, 32, 256, *tail)
     assert st == ck.CK_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------- the native host side's torch
+
+@pytest.fixture
+def bind(monkeypatch):
+    ck_build.build_all()
+    monkeypatch.setattr(ck, "_lib", None)
+    monkeypatch.setattr(ck, "_bind", None)
+    from rotated_w4a4_quantized_group_b200 import _ck_bind
+    return _ck_bind
+
+
+def test_the_native_host_side_serves_the_torch_it_was_built_for(bind):
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        ck.lib()
+    assert bind.torch_version == torch.__version__ and ck._bind is bind
+
+
+def test_the_native_host_side_is_left_out_with_another_torch(bind, monkeypatch):
+    monkeypatch.setattr(bind, "torch_version", "0.1")
+    with pytest.warns(UserWarning, match="built against torch 0.1"):
+        ck.lib()
+    assert ck._bind is None
+
+
+def test_the_native_host_side_is_built_again_for_another_torch(bind, monkeypatch, tmp_path):
+    """With a file for the extension that is newer than its sources."""
+    so, runs = tmp_path / "_ck_bind.so", []
+
+    def run(cmd, **kw):
+        runs.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(ck_build, "BIND", str(so))
+    monkeypatch.setattr(ck_build, "BUILD_DIR", str(tmp_path))
+    monkeypatch.setattr(ck_build.subprocess, "run", run)
+    for version, builds in ((torch.__version__, 1), (torch.__version__, 1), ("9.9", 2), ("9.9", 2), ("9.8", 3)):
+        monkeypatch.setattr(torch, "__version__", version)
+        ck_build.build_bind()
+        assert len(runs) == builds and so.exists()
+        assert f'-DCK_TORCH_VERSION="{version}"' in runs[-1]
 
 
 # ------------------------------------------------------------------- counts of tiles

@@ -304,7 +304,7 @@ size_t ck_fp4_scales_bytes(int64_t M, int64_t K, ck_fp4_format format, int n_exp
  *   scales        ck_fp4_scales_bytes(M, K, format, offsets ? n_experts : 0) bytes; the bytes of a
  *                 written tile past the last row and block are 0, tiles of no expert are not written
  * Errors: CK_ERR_INVALID_ARG, CK_ERR_UNSUPPORTED (M or K of 2^31 or more, or more than 2^31 - 1
- * tiles of 128 x 256), CK_ERR_CUDA.
+ * tiles of 128 x 128; with offsets these are M / 128 + n_experts rows of tiles), CK_ERR_CUDA.
  */
 ck_status ck_quant_fp4(const void* x, ck_dtype x_dtype, int64_t M, int64_t K, int64_t stride_m,
                        int64_t stride_k, ck_fp4_format format, const float* tensor_scale,

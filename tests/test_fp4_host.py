@@ -107,6 +107,22 @@ def test_negated_views_are_refused(launched):
     assert not launched
 
 
+# ------------------------------------------------------------------- limits
+
+@BOTH
+@pytest.mark.parametrize("M,K,E", [(2 ** 31 - 1, 128 * 130, 0), (2 ** 24 * 128 - 1, 128 * 128, 0),
+                                   (2 ** 24 * 128 - 128 * 1000, 128 * 128, 1000), (2 ** 30, 2 ** 15, 0)])
+def test_more_tiles_than_a_grid_are_refused(fmt, M, K, E):
+    """2^31 tiles of 128 x 128 and a few more, which are about half as many of 128 x 256."""
+    ck_build.build()
+    L, P = ck.lib(), 1 << 20
+    rows = M // 128 + E if E else -(-M // 128)
+    assert 2 ** 31 <= rows * (K // 128) < 1.02 * 2 ** 31
+    off = P if E else None
+    assert L.ck_quant_fp4(P, ck.CK_BF16, M, K, K, 1, fmt, None, off, E, P, K // 2, P, None) == ck.CK_ERR_UNSUPPORTED
+    assert L.ck_dequant_fp4(P, K // 2, P, M, K, fmt, None, off, E, P, ck.CK_BF16, K, None) == ck.CK_ERR_UNSUPPORTED
+
+
 # ------------------------------------------------------------------- addresses
 
 ODD = [("quant", dict(x=1)), ("quant", dict(dt=ck.CK_F32, x=2)), ("quant", dict(ts=2)), ("quant", dict(off=2, E=2)),

@@ -274,7 +274,10 @@ ck_status ck_rotate_quant_packed(const void* x, ck_dtype x_dtype, int64_t M, int
  *
  * Scale bytes are kept in tiles of 128 rows x 4 blocks, 512 bytes each, the order that the tensor
  * cores take: row r, block c of a tile at byte (r % 32) * 16 + (r / 32) * 4 + c; the tile of rows
- * 128 i.. and blocks 4 j.. at byte (i * ceil(blocks / 4) + j) * 512.  With rows sorted by expert
+ * 128 i.. and blocks 4 j.. at byte (i * ceil(blocks / 4) + j) * 512.  Bytes of a tile behind the last
+ * block of K must not be NaN (CK_MXFP4 0xFF; CK_NVFP4 0x7F, 0xFF): where K is not a multiple of 64 the
+ * products multiply them by zeros.  ck_quant_fp4 writes 0 there; tiles laid out by other means have to be
+ * cleared first.  Bytes of rows behind the last may be anything.  With rows sorted by expert
  * (offsets, below) expert e's rows start a tile row of their own, i = offsets[e] / 128 + e.
  * Scale pointers are 16-byte aligned; every other pointer of the fp4 calls is a multiple of its type's size
  * where nothing more is said (CK_ERR_INVALID_ARG otherwise).

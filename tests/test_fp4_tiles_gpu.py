@@ -150,6 +150,45 @@ def test_nan_stays_in_its_row_and_channel_of_a_pair(fmt):
     _close(out[keep], (xv @ wv[0].t())[keep], (xv.abs() @ wv[0].abs().t())[keep], K)
 
 
+# ------------------------------------------------------------------- bytes of tiles that stand for no block
+
+def _dirty(tiles, rows, blocks, fmt, seed):
+    """Scale tiles with other bytes where no block is: behind the last block anything but a NaN, in rows behind
+    the last anything."""
+    g = np.random.default_rng(seed)
+    any_byte, number = g.integers(0, 256, tiles.numel()), g.integers(0, 255, tiles.numel())
+    if fmt == NV:
+        number[number % 128 == 127] = 0x7E
+    wide, last = -(-blocks // 4) * 4, -(-rows // 128) * 128
+    out = any_byte.copy()
+    at = ref.tile_index(np.arange(rows), wide)
+    out[at] = number[at]
+    at = at[:, :blocks]
+    out[at] = tiles.cpu().numpy().reshape(-1)[at]
+    assert wide > blocks and last > rows and out.size == last * wide
+    return torch.from_numpy(out.astype(np.uint8)).view(tiles.shape).cuda()
+
+
+@FMT
+@pytest.mark.parametrize("want,M,N,steps", [(None, 5, 200, 1), (None, 9, 200, 6), ((0, 64), 40, 200, 6),
+                                            ((0, 64), 100, 907, 16), ((1, 64), 400, 1600, 4), (ONE, 900, 2100, 3),
+                                            (PAIR, 1500, 2178, 16)])
+def test_padding_of_scale_tiles_does_not_matter(fmt, want, M, N, steps):
+    """K ends one, two or three blocks into its last 64 (MX: one)."""
+    b = ref.BLOCK[fmt]
+    for K in (256 * steps + b * j for j in range(1, 64 // b)):
+        assert want is None or tile(M, N, K, fmt) == want
+        g = torch.Generator(device="cuda").manual_seed(K)
+        x = torch.randn(M, K, device="cuda", generator=g, dtype=BF16)
+        w, ws = ck.ck_quant_fp4(torch.randn(N, K, device="cuda", generator=g) * 0.05, fmt)
+        codes, xs = ck.ck_quant_fp4(x, fmt)
+        ws2, xs2 = _dirty(ws, N, K // b, fmt, 1), _dirty(xs, M, K // b, fmt, 2)
+        exact = ck.ck_fp4_linear(x, w, ws, fmt)
+        assert torch.equal(exact, ck.ck_fp4_linear(x, w, ws2, fmt))
+        assert torch.equal(exact, ck.ck_fp4_linear(codes, w, ws2, fmt, x_scales=xs2))
+        assert torch.equal(ck.ck_dequant_fp4(codes, xs, fmt), ck.ck_dequant_fp4(codes, xs2, fmt))
+
+
 # ------------------------------------------------------------------- by expert
 
 @FMT

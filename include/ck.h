@@ -269,7 +269,7 @@ ck_status ck_rotate_quant_packed(const void* x, ck_dtype x_dtype, int64_t M, int
  * negatives; the sign is bit 3 of the code), two to a byte with the even k in the low nibble.
  * Consecutive elements along K form blocks that share a scale byte:
  *   CK_MXFP4  32 elements; E8M0, 2^(byte - 127), 255 = NaN (OCP Microscaling Formats v1.0)
- *   CK_NVFP4  16 elements; E4M3, 0x7F = NaN, and one fp32 scale t for the whole tensor
+ *   CK_NVFP4  16 elements; E4M3 with the sign bit clear, 0x7F = NaN, and one fp32 scale t for the whole tensor
  * An element stands for code * scale (CK_MXFP4) or code * scale * t (CK_NVFP4).
  *
  * Scale bytes are kept in tiles of 128 rows x 4 blocks, 512 bytes each, the order that the tensor

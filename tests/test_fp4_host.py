@@ -123,6 +123,17 @@ def test_more_tiles_than_a_grid_are_refused(fmt, M, K, E):
     assert L.ck_dequant_fp4(P, K // 2, P, M, K, fmt, None, off, E, P, ck.CK_BF16, K, None) == ck.CK_ERR_UNSUPPORTED
 
 
+@BOTH
+def test_more_channels_than_few_rows_take_are_refused(fmt):
+    """Rows quantized inside: 65535 tiles of 128 channels."""
+    ck_build.build()
+    L, P = ck.lib(), 1 << 20
+    N = 65535 * 128 + 1
+    for M, K in ((1, 64), (16, 2048)):
+        assert L.ck_fp4_linear(P, ck.CK_BF16, M, K, K, 1, fmt, None, None, P, N, K // 2, P, None, None, 0, P, ck.CK_BF16, N,
+                               None, 0, None, None) == ck.CK_ERR_UNSUPPORTED
+
+
 # ------------------------------------------------------------------- addresses
 
 ODD = [("quant", dict(x=1)), ("quant", dict(dt=ck.CK_F32, x=2)), ("quant", dict(ts=2)), ("quant", dict(off=2, E=2)),

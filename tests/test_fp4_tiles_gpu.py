@@ -150,6 +150,31 @@ def test_nan_stays_in_its_row_and_channel_of_a_pair(fmt):
     _close(out[keep], (xv @ wv[0].t())[keep], (xv.abs() @ wv[0].abs().t())[keep], K)
 
 
+@FMT
+@pytest.mark.parametrize("M,N,K", [(1, 28677, 4096), (8, 40000, 1040), (16, 20001, 2064), (3, 151936, 272), (2, 30000, 16400)])
+def test_few_rows_of_many_channels(fmt, M, N, K):
+    """More tiles of 128 channels than run at once, the rows quantized in each.  The weights are quantized and
+    read back by the library, bit for bit what the reference gives."""
+    K = width(K, fmt)
+    assert ck.fp4_workspace_bytes(M, K, fmt) == 0                # quantized inside
+    g = torch.Generator(device="cuda").manual_seed(N)
+    w, ws = ck.ck_quant_fp4(torch.randn(N, K, device="cuda", generator=g) * 0.05, fmt)
+    x = _x(M, K, F32, 106, spread=False)
+    bias = torch.randn(N, device="cuda", generator=g)
+    buf = torch.full((M + 2, N + 3), 7.25, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = ck.ck_fp4_linear(x.cuda(), w, ws, fmt, bias, out=buf[1:1 + M, 1:1 + N], dev_status=status)
+    assert status.item() == 0
+    xv = _xvalues(x, fmt, None)
+    for lo in range(0, N, 32768):                                # in 64 bits, some channels at a time
+        n = slice(lo, min(lo + 32768, N))
+        wv = ck.ck_dequant_fp4(w, ws, fmt, out_dtype=F32)[n].double()
+        b = bias[n].double()
+        _close(out[:, n], xv @ wv.t() + b, xv.abs() @ wv.abs().t() + b.abs(), K, f"channels from {lo}")
+    buf[1:1 + M, 1:1 + N] = 7.25
+    assert (buf == 7.25).all()
+
+
 # ------------------------------------------------------------------- bytes of tiles that stand for no block
 
 def _dirty(tiles, rows, blocks, fmt, seed):

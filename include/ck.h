@@ -280,7 +280,7 @@ ck_status ck_rotate_quant_packed(const void* x, ck_dtype x_dtype, int64_t M, int
  * cleared first.  Bytes of rows behind the last may be anything.  With rows sorted by expert
  * (offsets, below) expert e's rows start a tile row of their own, i = offsets[e] / 128 + e.
  * Scale pointers are 16-byte aligned; every other pointer of the fp4 calls is a multiple of its type's size
- * where nothing more is said (CK_ERR_INVALID_ARG otherwise).
+ * where nothing more is said (CK_ERR_INVALID_ARG otherwise).  No output may overlap an input.
  */
 typedef enum { CK_MXFP4 = 0, CK_NVFP4 = 1 } ck_fp4_format;
 

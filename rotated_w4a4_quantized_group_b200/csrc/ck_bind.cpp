@@ -1,10 +1,11 @@
 // ck_bind.cpp -- the fp4 calls from torch tensors without Python's share of the host time.
 //
 // Each function takes the tensors of the ck.py function of its name, in order.  Where they are what
-// the call wants, it allocates what was not given, calls the library on torch's current stream and
-// returns the result (or the library's status, an int, if that is not CK_OK).  Anything else, a wrong
-// type or size, another current device, an allocation that fails, makes it return None with nothing
-// done: ck.py then goes through its own checks, which say what is wrong or handle the case.
+// the call wants, it allocates its outputs and workspace (the products take given ones too), calls the
+// library on torch's current stream and returns the result (or the library's status, an int, if that is
+// not CK_OK).  Anything else, a wrong type or size, another current device, an allocation that fails, the
+// quantizer's given codes or scales or rows of codes that are not whole 16 bytes, makes it return None with
+// nothing done: ck.py then goes through its own checks, which say what is wrong or handle the case.
 // A call costs about 2 us here that Python's checks and ctypes take 9 for.
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>

@@ -248,8 +248,8 @@ struct Fp4Scale {
 //     rounded correctly (reciprocal, one residual, one correction: see RowDivisor): off a border it
 //     is at least 2^-24 of it away, so its rounding never moves it onto one.  d = fl(s t) has 24
 //     bits.  There 16-bit values take x * (1 / d), moved where a border falls on or next to one of them
-//     (see fp4_moves); fp32 values the rounded quotient, and, where that is on a border, the quotient
-//     rounded to odd.
+//     (see fp4_moves); fp32 values the rounded quotient, and, in a block where one lies on a multiple of
+//     1/4, as every border does, the quotient rounded to odd.
 template <typename T, bool NV, bool HAS_T>
 __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, const Fp4Tensor& p) {
     constexpr int GRID = GridBits<T>::value;
@@ -345,7 +345,9 @@ __device__ __forceinline__ void fp4_codes(const float (&x)[16], const Fp4Scale& 
     if (b.mode == 1) {
         const unsigned long long r2 = f2_pack(b.r, b.r), nd2 = f2_pack(-b.d, -b.d);
         // A quotient on a border may have been rounded there.  All borders are multiples of 1/4:
-        // adding and taking away 1.5 * 2^21 rounds to those, and what changes nothing is one (or zero).
+        // adding and taking away 1.5 * 2^21 rounds to those, and what changes nothing is one: a border, but
+        // also zero and the codes' own values, whose blocks take the slow way for nothing (4096 x 16384 fp32
+        // under a tensor scale: 49 us without, 66 with one value in a hundred zero).
         const unsigned long long big = f2_pack(0x1.8p21f, 0x1.8p21f);
         float least = 1.0f;
 #pragma unroll

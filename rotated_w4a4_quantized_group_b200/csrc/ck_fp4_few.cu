@@ -399,7 +399,10 @@ bool fp4_few_takes(int64_t M, int64_t N, int64_t K, bool nv, bool ragged) {
 
 // Rows x steps of 256 k up to which the tiles quantize for themselves.  Measured (3840 channels, replayed,
 // bf16): K = 3840, 8 rows: MX 6.5 us and NV 7.3 against 7.3 and 7.9 with the quantizer in a launch of its
-// own; 16 rows: 8.1 and 9.7 against 7.3 and 7.9; but that launch also costs the host 3 us.
+// own; 16 rows: 8.1 and 9.7 against 7.3 and 7.9; but that launch also costs the host 3 us.  The channels do
+// not count, though every tile quantizes the rows again: with more tiles than run at once, 4096 k to MX, 1
+// row takes 21 us for 28672 channels (the weights alone 9.7) and 80 for 151936 (51), 8 rows 28 and 116, where
+// 16 rows, quantized by a launch of their own, take 16 for 28672.
 bool fp4_few_fuses(int64_t M, int64_t K) {
     return M >= 1 && M <= 16 && M * ((K + fp4f::BK - 1) / fp4f::BK) <= 180;
 }

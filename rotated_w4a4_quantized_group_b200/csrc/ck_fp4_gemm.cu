@@ -18,9 +18,12 @@
 //            MMAs that read them) and issues the MMAs: the CTA of rank 0 for both CTAs
 //   warps 4-11  the epilogue: two warps per lane quarter on alternate 32-row chunks, from one of
 //            two accumulators while the MMAs fill the other
-// Measured (graph-replayed, the product alone): 8192 x 3840 x 3840 NV 54.8 us (4.4 PFLOP/s; tensor pipe
-// 60% of active cycles, 1.63 GHz at the power cap), 8192 x 10240 x 3840 MX 116 us (5.5 PFLOP/s); a stage
-// takes 547 (NV) or 476 (MX) cycles where its MMAs alone need 384.
+// Measured (graph-replayed, the product alone, by box): 8192 x 3840 x 3840 NV 54 to 56 us (4.3 to 4.5
+// PFLOP/s; tensor pipe 60% of active cycles, 1.63 GHz at the power cap), 8192 x 10240 x 3840 MX 116 to 120
+// us (5.4 to 5.5 PFLOP/s); a stage takes 547 (NV) or 476 (MX) cycles where its MMAs alone need 384.  What
+// holds it there is not settled: no change to how a stage is issued shortened it, and both formats, as the
+// one-CTA tile of 128 rows, come to 64 to 67 bytes a cycle into an SM's shared memory, a bound that no
+// measurement with fewer bytes has tested.
 // Every wait is bounded; a CTA leaves only after its own copies have landed, the MMAs that read
 // its memory have completed and the arrivals that were sent to it have come.
 #include <cuda.h>
@@ -323,8 +326,8 @@ __global__ void __launch_bounds__(fp4g::THREADS, 1)
         __syncwarp();
     } else if (warp == WARP_MMA && rank == 0) {
         // ---------------------------------------------------------------- MMA issuer
-        // One elected thread walks the ring.  What it executes per stage is what bounds large
-        // products, so the loop only adds to the low words of its descriptors.
+        // One elected thread walks the ring; the loop only adds to the low words of its descriptors
+        // (8192 x 3840 x 3840 NV: 60 -> 58 us).
         if (elect_one()) {
             grid_dependency_wait();
             const uint32_t slot_step = p.stage_bytes >> 4;   // descriptors count 16-byte units

@@ -5,9 +5,10 @@
 //   dequantize: value = cvt(fl(fl(code * scale) * t))
 //
 // Both are one pass over memory: K * sizeof(x) + K / 2 + K / block bytes a row, 12.5 us for 8192 x 3840
-// bf16 at the measured copy rate.  Measured there: MX 15.2 us, NV with a tensor scale 20 to 22 (about 206
-// instructions a thread and block, of them 50 for the scale: the integer pipe is 61% busy), back 13.9;
-// 4096 x 16384 fp32: NV 49 us (48 at the copy rate), column-major 55, back 51.
+// bf16 at the measured copy rate.  Measured there: MX 15.2 us, NV with a tensor scale 20 to 22 (about 202
+// instructions a thread and block, of them 50 for the scale; the integer pipe is 60% busy, issue 64%, and a
+// warp waits most for its loads), back 13.9 to 14.3; 4096 x 16384 fp32: NV 49 us (48 at the copy rate),
+// column-major 55, back 51.
 // A CTA takes 128 rows x 128 channels, so that it owns whole 512-byte scale tiles and writes each
 // of them as one contiguous run from shared memory; a thread takes sixteen channels of a row (an
 // NV block, or half an MX block whose other half is its neighbour lane's), with the loads of
